@@ -292,6 +292,120 @@ moe_status moe_dequant_rows(const moe_qmat *m, int32_t expert, int32_t row0, int
 moe_status moe_router_topk_static(const uint16_t *x, int32_t T, int32_t H, const float *Wr, const float *bias,
                                   int32_t E, int32_t k, int32_t *idx, float *w, float *logits_opt, void *stream);
 
+/* ------------------------------------------------------------------ block operators
+ * What a block needs around its experts, for serving and for training: the norms that close one
+ * block and open the next, the (token, slot) pairs sorted by expert and collected again, each with
+ * its gradient, and MXFP4 rows with their product per expert. Values are fp32, fp16 or bf16 (a
+ * MOE_F32 / MOE_F16 / MOE_BF16 argument names the type of the tensor before it); gains, gates,
+ * routing weights and statistics are fp32, sums are carried in fp32 and a result is rounded once, to
+ * nearest even. Results are the same in every run. The conventions above hold; shape rules: H, K
+ * and N multiples of 64 up to 16384 (a multiple of 32 gives MOE_ERR_UNSUPPORTED, anything else
+ * MOE_ERR_INVALID_ARG), 1 <= k <= min(E, 32), E <= 4096, T * k < 2^31. Outputs do not overlap inputs
+ * unless said so. */
+enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+
+/* Bytes of device workspace that suffice for every block operator on T tokens with k slots, E
+ * experts and rows of H values (0 for sizes they do not take). A workspace serves one stream at a
+ * time; initialise it with moe_workspace_init. */
+size_t moe_block_workspace_bytes(int32_t T, int32_t k, int32_t E, int32_t H);
+
+/* The norms around a block:
+ *   z  = gate * post_gain * N(y)     N(v) = v / sqrt(mean_h v_h^2 + eps); post_norm = 0: y for N(y)
+ *   r' = res_scale * r + z
+ *   u  = pre_gain * N(r')            of r' before its rounding
+ * y NULL: r' = res_scale * r (a stack's first norm; post_norm, post_gain, gate, rstd_y unused). u NULL:
+ * no second norm. gate fp32: [H] (MOE_GATE_CHANNEL) or [T] (MOE_GATE_TOKEN); gains fp32 [H]; a NULL
+ * gain or MOE_GATE_NONE is 1. r, r_out [T,H] of r_type (r_out may be r, or NULL); y [T,H] of y_type; u
+ * [T,H] of u_type; rstd_y, rstd_u fp32 [T] or NULL: the two norms' 1 / sqrt(...), which the gradient
+ * needs. */
+moe_status moe_block_norm(const void *r, int32_t r_type, const void *y, int32_t y_type, int32_t T, int32_t H,
+                          int32_t post_norm, const float *post_gain, const float *gate, int32_t gate_mode,
+                          float res_scale, float eps, const float *pre_gain, void *r_out, void *u, int32_t u_type,
+                          float *rstd_y, float *rstd_u, void *stream);
+
+/* Gradient of moe_block_norm. dr_out [T,H] of r_type and du [T,H] of u_type: the gradients that reach
+ * r' and u (either NULL: none does; not both); r_out: r' as the forward pass stored it; rstd_u (needed
+ * with du) and rstd_y (needed with y and post_norm) as it returned them. With y the gradient of r' is
+ *   g = dr_out + rstd_u (h - x mean(h x)),  h = du pre_gain,  x = r' rstd_u
+ * dr = res_scale g (of r_type; may be dr_out); dy of y_type (NULL without y);
+ * d_post_gain, d_pre_gain fp32 [H] and d_gate fp32 ([H] or [T]): each may be NULL. d_gate and
+ * d_post_gain need y, d_gate a gate, d_pre_gain du. T = 0 sets d_post_gain, d_pre_gain and a
+ * channel gate's d_gate to zero. */
+moe_status moe_block_norm_backward(const void *dr_out, const void *du, int32_t u_type, const void *r_out,
+                                   int32_t r_type, const float *rstd_u, const void *y, int32_t y_type,
+                                   const float *rstd_y, int32_t T, int32_t H, int32_t post_norm,
+                                   const float *post_gain, const float *gate, int32_t gate_mode, float res_scale,
+                                   const float *pre_gain, void *dr, void *dy, float *d_post_gain, float *d_gate,
+                                   float *d_pre_gain, void *ws, size_t ws_bytes, void *stream);
+
+/* The T * k (token, slot) pairs sorted by (expert, token, slot), as moe_permute does it but without a
+ * copy of the tokens, and with pairs that take no expert: idx[t,j] = -1 (a padded token, a slot over an
+ * expert's capacity).
+ *   counts[e]  pairs of expert e;  offsets[0..E] their exclusive scan, offsets[E] = kept pairs
+ *   row_of     [T,k] place of each pair, -1 for a pair without an expert
+ *   src        [T*k] token of the pair at each row, -1 from row offsets[E] on
+ * idx int32 [T,k] in [-1, E); other values count as -1 and record MOE_ERR_DEVICE_CHECK. T = 0 sets
+ * counts and offsets to zero. */
+moe_status moe_sort_pairs(const int32_t *idx, int32_t T, int32_t k, int32_t E, int32_t *counts, int32_t *offsets,
+                          int32_t *row_of, int32_t *src, void *ws, size_t ws_bytes, void *stream);
+
+/* Tokens to their pairs' rows: rows[row_of[t,j],:] = x[t,:]. x [T,H] and rows [T*k,H] of one type.
+ * kept: device pointer to the number of kept pairs (offsets + E): rows from there on become zero;
+ * NULL: they are left as they were. Entries of row_of outside [0, T*k) are skipped, here and below. */
+moe_status moe_dispatch(const void *x, int32_t type, int32_t T, int32_t k, int32_t H, const int32_t *row_of,
+                        const int32_t *kept, void *rows, void *stream);
+
+/* Rows back to their tokens: y[t,:] = sum_j w[t,j] rows[row_of[t,j],:] + residual[t,:], in j order.
+ * rows [T*k,H] of `type`; w fp32 [T,k], NULL = 1 (the gradient of moe_dispatch); residual fp32 [T,H] or
+ * NULL (may be y); y [T,H] of y_type. A pair without a row adds nothing, whatever its weight. */
+moe_status moe_collect(const void *rows, int32_t type, int32_t T, int32_t k, int32_t H, const int32_t *row_of,
+                       const float *w, const float *residual, void *y, int32_t y_type, void *stream);
+
+/* Gradient of moe_collect for dy [T,H] of dy_type (the residual's gradient is dy itself):
+ *   d_rows[row_of[t,j],:] = w[t,j] dy[t,:]   of `type` (rows from *kept on become zero, as moe_dispatch)
+ *   d_w[t,j] = sum_h dy[t,h] rows[row_of[t,j],h]   fp32, 0 for a pair without a row
+ * Either output may be NULL; rows may be NULL without d_w, and d_rows may be rows itself. */
+moe_status moe_collect_backward(const void *dy, int32_t dy_type, const void *rows, int32_t type, int32_t T, int32_t k,
+                                int32_t H, const int32_t *row_of, const float *w, const int32_t *kept, void *d_rows,
+                                float *d_w, void *stream);
+
+/* MXFP4 rows (the OCP microscaling format): blocks of 32 values along K, each value an e2m1 code (bit
+ * 3 the sign; 0 0.5 1 1.5 2 3 4 6 for bits 0-2) times 2^(b-127) of the block's scale byte b (255: NaN).
+ *   codes  uint8 [rows][K/2]   value 2i in the low, 2i+1 in the high four bits of byte i
+ *   scales uint8 [rows][K/32] */
+typedef struct moe_mx4_mat {
+  int32_t n_experts;
+  int32_t rows;             /* per expert */
+  int32_t K;
+  const uint8_t *codes;     /* [n_experts][rows][K/2] */
+  const uint8_t *scales;    /* [n_experts][rows][K/32] */
+} moe_mx4_mat;
+
+/* Rows to MXFP4: b = max(floor(log2(max |x|)) - 2 + 127, 0) over each block, the code nearest to
+ * x 2^(127-b), ties to the even code, magnitudes over 6 to 6. A block that holds a NaN or an infinity
+ * gets b = 255. x [T,K] of `type`. row_of NULL: row t of codes and scales is x[t]. row_of int32 [T,k]:
+ * x[t] goes to each row row_of[t,j] of the T*k rows (moe_dispatch of the quantised rows, each token
+ * quantised once); kept as in moe_dispatch (codes and scales become zero). */
+moe_status moe_mx4_quantize(const void *x, int32_t type, int32_t T, int32_t K, const int32_t *row_of, int32_t k,
+                            const int32_t *kept, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* MXFP4 rows back: out [rows,K] of `type`. Exact in fp32 and bf16 down to their subnormals. */
+moe_status moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t K, void *out,
+                              int32_t type, void *stream);
+
+/* Product of MXFP4 rows with per-expert MXFP4 weights, fp32 accumulation:
+ *   out[r,n] = sum_k A[r,k] W_g[n,k]                     for the rows offsets[g] <= r < offsets[g+1]
+ *   out[r,n] = silu(A W_g^T)[r,n] * (A U_g^T)[r,n]       with up != NULL (gate and up projections)
+ * a_codes / a_scales: n_rows rows; w (and up): n_experts = E experts of N = rows features; offsets
+ * device int32 [E+1], offsets[0] = 0, monotone, offsets[E] <= n_rows (rows behind offsets[E] become
+ * zero); NULL with E = 1: one group of all rows. out [n_rows,N] fp16 or bf16 (MOE_ERR_UNSUPPORTED for
+ * fp32: the tensor cores' sums do not carry that precision). ws: its control area alone, for the error
+ * word (MOE_ERR_TIMEOUT). */
+moe_status moe_mx4_product(const uint8_t *a_codes, const uint8_t *a_scales, int32_t n_rows, const int32_t *offsets,
+                           int32_t E, const moe_mx4_mat *w, const moe_mx4_mat *up, void *out, int32_t out_type,
+                           void *ws, size_t ws_bytes, void *stream);
+
 /* Per-kernel device timing, off by default. While enabled, the library records a pair of CUDA
  * events on the launching stream around every kernel it launches (from the calling host thread;
  * not for use during CUDA-graph capture) and keeps them in a process-wide list. Enabling (on = 1)

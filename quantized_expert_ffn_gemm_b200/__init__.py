@@ -5,7 +5,8 @@ supplies device memory and the current CUDA stream. If the shared library is mis
 be loaded, importing works but every call raises (there is no fallback path).
 
 Entry points mirror include/moe_ffn.h: rmsnorm_bf16, router_topk, permute, expert_ffn, combine,
-layer_forward, stack_forward, dequant_rows, read_device_error, plus a Workspace helper.
+layer_forward, stack_forward, dequant_rows, read_device_error, plus a Workspace helper; the block
+operators (norms around a block, sorted pairs, their gradients, MXFP4) are in block.py.
 """
 from __future__ import annotations
 
@@ -14,6 +15,11 @@ import os
 from typing import Optional, Sequence
 
 import torch
+
+from . import block as _block
+from .block import (BF16, F16, F32, GATE_CHANNEL, GATE_NONE, GATE_TOKEN, Mx4, block_norm, block_norm_backward,  # noqa: F401
+                    block_workspace_bytes, collect, collect_backward, dispatch, mx4_dequantize, mx4_product,
+                    mx4_quantize, sort_pairs)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_ffn.so")
@@ -27,7 +33,7 @@ EXPORTED = ["moe_status_string", "moe_workspace_bytes", "moe_workspace_init", "m
             "moe_router_topk", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
             "moe_stack_forward", "moe_dequant_rows", "moe_read_device_error", "moe_timing_enable",
             "moe_timing_read", "moe_kernel_count", "moe_kernel_name", "moe_router_topk_static",
-            "moe_test_wait_timeout", "moe_layer_forward_host", "moe_stack_forward_host"]
+            "moe_test_wait_timeout", "moe_layer_forward_host", "moe_stack_forward_host"] + _block.EXPORTED
 
 
 class MoeError(RuntimeError):
@@ -68,6 +74,7 @@ def lib():
         _lib.moe_workspace_bytes.argtypes = [ctypes.POINTER(LayerDesc), ctypes.c_int32]
         for name in EXPORTED[2:]:
             getattr(_lib, name).restype = ctypes.c_int32
+        _block.bind(_lib)
         _lib.moe_kernel_name.restype = ctypes.c_char_p
         _lib.moe_kernel_name.argtypes = [ctypes.c_int32]
     return _lib
