@@ -4,8 +4,7 @@
 //
 //   quantise   b = max(floor(log2(max |x|)) - 2 + 127, 0);  code = nearest e2m1 of x 2^(127 - b), ties to
 //              the even code, magnitudes over 6 become 6; a block with a NaN or an infinity reads back NaN
-//   product    out[r, n] = sum_k A[r, k] W_g[n, k] for every row r of group g, or, with an up matrix,
-//              silu(A W_g^T) * (A U_g^T)
+//   (the product of such rows is in mx4_product.cu)
 //
 // floor(log2) of an fp32 value is its exponent field less 127, and scaling by a power of two is exact, so
 // quantising rounds once, at the code.
@@ -92,51 +91,6 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *__re
   }
 }
 
-// A plain product: one warp a row and 32 output features (a lane each).
-__global__ void __launch_bounds__(256) mx4_product_kernel(const Mx4ProductArgs a) {
-  const int lane = threadIdx.x & 31, n_seg = a.N / 32, kb = a.K / 32;
-  const long long n_items = (long long)a.n_rows * n_seg, stride = (long long)gridDim.x * 8;
-  for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < n_items; it += stride) {
-    const int row = (int)(it / n_seg), n = (int)(it % n_seg) * 32 + lane;
-    int g = 0;
-    if (a.offsets) {  // the last group that starts at or before the row
-      int lo = 0, hi = a.E;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.offsets[mid] <= row) lo = mid;
-        else hi = mid - 1;
-      }
-      g = lo;
-    }
-    float acc = 0.0f, acc_up = 0.0f;
-    if (g < a.E) {
-      const size_t wr = (size_t)g * a.N + n;
-      for (int b = 0; b < kb; ++b) {
-        const uint32_t *ac = reinterpret_cast<const uint32_t *>(a.a_codes + ((size_t)row * kb + b) * 16);
-        const uint32_t *wc = reinterpret_cast<const uint32_t *>(a.w_codes + (wr * kb + b) * 16);
-        const uint32_t *uc = reinterpret_cast<const uint32_t *>(a.up_codes + (wr * kb + b) * 16);
-        float s = 0.0f, su = 0.0f;
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t ca = ac[q], cw = wc[q], cu = a.up_codes ? uc[q] : 0u;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float va = e2m1_value((ca >> (4 * i)) & 15u);
-            s = fmaf(va, e2m1_value((cw >> (4 * i)) & 15u), s);
-            su = fmaf(va, e2m1_value((cu >> (4 * i)) & 15u), su);
-          }
-        }
-        const float da = e8m0_to_float(a.a_scales[(size_t)row * kb + b]);
-        acc = fmaf(s * da, e8m0_to_float(a.w_scales[wr * kb + b]), acc);
-        if (a.up_codes) acc_up = fmaf(su * da, e8m0_to_float(a.up_scales[wr * kb + b]), acc_up);
-      }
-    }
-    if (a.up_codes) acc = acc / (1.0f + expf(-acc)) * acc_up;
-    const size_t o = (size_t)row * a.N + n;
-    if (a.out_type == MOE_F16) static_cast<__half *>(a.out)[o] = __float2half_rn(acc);
-    else static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(acc);
-  }
-}
-
 int thread_grid(long long n) {
   const long long want = (n + 255) / 256, cap = (long long)num_sms() * 16;
   return (int)(want < cap ? want : cap);
@@ -157,13 +111,6 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, l
   KTimer kt_(KID_MX4_DEQUANTIZE, s);
   const long long n = rows * (K / 8);
   mx4_dequantize_kernel<<<thread_grid(n), 256, 0, s>>>(codes, scales, n, out, type);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_mx4_product(const Mx4ProductArgs &a, cudaStream_t s) {
-  KTimer kt_(KID_MX4_PRODUCT, s);
-  const long long items = (long long)a.n_rows * (a.N / 32), want = (items + 7) / 8, cap = (long long)num_sms() * 16;
-  mx4_product_kernel<<<(int)(want < cap ? want : cap), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

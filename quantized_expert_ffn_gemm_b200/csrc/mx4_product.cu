@@ -1,0 +1,431 @@
+// Product of MXFP4 rows with per-expert MXFP4 weights on the block-scaled tensor cores:
+//
+//   out[r, n] = sum_k A[r, k] W_g[n, k]   for the rows r of group g, or, with an up matrix,
+//   out[r, n] = silu(A W_g^T)[r, n] * (A U_g^T)[r, n]
+//
+// tcgen05.mma kind::mxf4 multiplies e2m1 codes and applies both operands' block scales itself (one e8m0
+// byte for 32 values, read from tensor memory), so the codes go from HBM to shared memory by TMA and from
+// there to the MMA untouched; only the scale bytes are rearranged on the way.
+//
+//   tile    128 rows of a group (MMA M, one tensor-memory lane a row) x NC columns: NC features, or NC / 2
+//           gate and NC / 2 up rows of the same features, whose accumulators one thread holds side by side
+//   stage   K = 256: 128 bytes of codes a row (one 128-byte swizzle row), four MMAs of K = 64
+//   scales  per 128 rows and K = 128 one 512-byte block, row r's four bytes at (r % 32) 16 + (r / 32) 4;
+//           tcgen05.cp puts it into 4 columns of all four lane quarters. An MMA reads bytes 0-1 or 2-3.
+//   TMEM    two accumulators of NC columns and two sets of a stage's scales. NC = 256 leaves 48 columns
+//           for the scales if the accumulators (columns 0 and 208) share 48: a tile's epilogue
+//           reads the shared ones first and then lets the next tile begin.
+//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warps 4-7 epilogue, warps 8-11 scales.
+//
+// Tiles are dealt round-robin with a group's row tiles innermost, so a weight tile is read from HBM once and
+// by the group's other row tiles from L2. Every wait is bounded and reports MOE_ERR_TIMEOUT.
+#include "block.cuh"
+#include "tc.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMxThreads = 384;
+constexpr int kMxRows = 128;     // rows of a tile
+constexpr int kMxBoxRows = 32;   // rows of one TMA box of A: a short tile loads only the boxes it has rows in
+constexpr int kMxStageK = 256;   // K of a stage
+constexpr int kMxRowBytes = kMxStageK / 2;
+constexpr uint32_t kMxAcc1 = 208;  // column of the second accumulator
+constexpr uint32_t kMxSf = 464;    // columns of the scales: two sets of 24
+
+template <int NC>
+struct MxSmem {
+  static constexpr int kA = kMxRows * kMxRowBytes, kB = NC * kMxRowBytes;
+  static constexpr int kRowBlocks = (NC + 127) / 128;               // 128-row scale blocks of B
+  static constexpr int kSfA = 2 * 512, kSfB = 2 * kRowBlocks * 512;  // two K = 128 blocks a stage
+  static constexpr int kStage = kA + kB + kSfA + kSfB;
+  static constexpr int kStages = NC == 256 ? 4 : NC == 128 ? 5 : 7;
+  static constexpr int kBar = kStages * kStage;
+  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kPrefix = kBar + (kNumBars * 8 + 16 + 15) / 16 * 16;
+  static constexpr int bytes(int E) { return kPrefix + (E + 1) * 4 + 1024; }
+  static_assert(kStage % 1024 == 0, "stages start on swizzle atoms");
+};
+
+struct MxArgs {
+  const int32_t *offsets;
+  const uint8_t *a_scales, *w_scales, *up_scales;
+  void *out;
+  int out_type, n_rows, K, N, E, n_tiles_n;
+  Ctrl *ctrl;
+};
+
+struct MxTile {
+  int group, row0, rows, n0;
+};
+
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+// one 512-byte scale block (32 rows of 16 bytes) to 4 columns, repeated in the four lane quarters
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// unswizzled K-major descriptor: 8-row core matrices of 128 bytes one behind the other
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1u << 46);
+}
+// kind::mxf4: A and B e2m1, scales ue8m0, both K-major, M = 128; sf: byte of the scale word (0 or 2)
+__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 7) << 27) |
+         (sf << 29);
+}
+__device__ __forceinline__ void mx_ld16(uint32_t taddr, uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void mx_timeout(Ctrl *ctrl, int where) { set_device_error(ctrl, MOE_ERR_TIMEOUT, where); }
+
+// start and end row of a group, whatever the offsets hold: 0 <= start <= end <= n_rows
+__device__ __forceinline__ int2 mx_group(const MxArgs &a, int g) {
+  if (!a.offsets) return make_int2(0, a.n_rows);
+  const int s = min(max(__ldg(a.offsets + g), 0), a.n_rows);
+  return make_int2(s, min(max(__ldg(a.offsets + g + 1), s), a.n_rows));
+}
+
+template <int NC, bool UP>
+__global__ void __launch_bounds__(kMxThreads, 1)
+mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_u, const MxArgs args) {
+  using S = MxSmem<NC>;
+  constexpr int kStages = S::kStages, kFeat = UP ? NC / 2 : NC;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *gbase = smem_raw + (base - smem_u32(smem_raw));
+  auto st_a = [&](int s) { return base + s * S::kStage; };
+  auto st_b = [&](int s) { return base + s * S::kStage + S::kA; };
+  auto st_sf = [&](int s) { return base + s * S::kStage + S::kA + S::kB; };
+  auto full = [&](int s) { return base + S::kBar + 8u * s; };
+  auto empty = [&](int s) { return base + S::kBar + 8u * (kStages + s); };
+  auto acc_full = [&](int b) { return base + S::kBar + 8u * (2 * kStages + b); };
+  auto acc_empty = [&](int b) { return base + S::kBar + 8u * (2 * kStages + 2 + b); };
+  const uint32_t acc_over = base + S::kBar + 8u * (2 * kStages + 4);  // the shared columns are read
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + S::kBar + S::kNumBars * 8);
+  int32_t *s_pref = reinterpret_cast<int32_t *>(gbase + S::kPrefix);  // [E + 1] tiles before a group
+  __shared__ int32_t s_warp[kMxThreads / 32];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Ctrl *ctrl = args.ctrl;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1 + 4);  // TMA's bytes, the scale warps
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 4);
+    }
+    mbar_init(acc_over, 4);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  {  // tiles before each group: every thread sums a run of groups, then a block scan of the runs
+    const int per = (args.E + kMxThreads - 1) / kMxThreads, g0 = tid * per, g1 = min(args.E, g0 + per);
+    int mine = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int2 r = mx_group(args, g);
+      if (args.offsets && (r.x != args.offsets[g] || r.y != args.offsets[g + 1] || (g == 0 && r.x != 0)))
+        set_device_error(ctrl, MOE_ERR_DEVICE_CHECK, g);
+      mine += (r.y - r.x + kMxRows - 1) / kMxRows * args.n_tiles_n;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int run = incl - mine;
+    for (int w = 0; w < warp; ++w) run += s_warp[w];
+    for (int g = g0; g < g1; ++g) {
+      const int2 r = mx_group(args, g);
+      s_pref[g] = run;
+      run += (r.y - r.x + kMxRows - 1) / kMxRows * args.n_tiles_n;
+    }
+    if (tid == kMxThreads - 1) s_pref[args.E] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = s_pref[args.E], G = gridDim.x, nk = (args.K + kMxStageK - 1) / kMxStageK;
+  const int n_my = total > (int)blockIdx.x ? (total - (int)blockIdx.x + G - 1) / G : 0;
+
+  auto tile_at = [&](int tl) {
+    const int ti = blockIdx.x + tl * G;
+    int lo = 0, hi = args.E - 1;  // the last group that starts at or before the tile and has one
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pref[mid] <= ti) lo = mid;
+      else hi = mid - 1;
+    }
+    const int mt = (s_pref[lo + 1] - s_pref[lo]) / args.n_tiles_n, local = ti - s_pref[lo];
+    const int2 r = mx_group(args, lo);
+    MxTile t;
+    t.group = lo;
+    t.row0 = r.x + (local % mt) * kMxRows;
+    t.rows = min(kMxRows, r.y - t.row0);
+    t.n0 = (local / mt) * kFeat;
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0;
+      for (int tl = 0; tl < n_my && ok; ++tl) {
+        const MxTile t = tile_at(tl);
+        const int nbox = (t.rows + kMxBoxRows - 1) / kMxBoxRows, wrow = t.group * args.N + t.n0;
+        const uint32_t tx = (uint32_t)(nbox * kMxBoxRows + NC) * kMxRowBytes;
+        for (int ks = 0; ks < nk; ++ks, ++g) {
+          const int s = g % kStages;
+          if (!mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u)) {
+            mx_timeout(ctrl, 41);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full(s), tx);
+          for (int b = 0; b < nbox; ++b)
+            tma_load_2d(st_a(s) + b * kMxBoxRows * kMxRowBytes, &tm_a, ks * kMxRowBytes, t.row0 + b * kMxBoxRows, full(s));
+          tma_load_2d(st_b(s), &tm_w, ks * kMxRowBytes, wrow, full(s));
+          if (UP) tma_load_2d(st_b(s) + kFeat * kMxRowBytes, &tm_u, ks * kMxRowBytes, wrow, full(s));
+        }
+      }
+      // after a give-up somewhere: the copies of the last stages have landed before the CTA leaves
+      for (int j = max(0, g - kStages); j < g; ++j) (void)mbar_wait(full(j % kStages), (uint32_t)(j / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t id0 = idesc_mxf4(NC, 0), id2 = idesc_mxf4(NC, 2);
+      bool ok = true;
+      int g = 0;
+      for (int tl = 0; tl < n_my && ok; ++tl) {
+        const int b = tl & 1;
+        if (!mbar_wait(acc_empty(b), (((uint32_t)tl >> 1) & 1u) ^ 1u) ||
+            (NC > (int)kMxAcc1 && tl > 0 && !mbar_wait(acc_over, (uint32_t)(tl - 1) & 1u))) {
+          mx_timeout(ctrl, 42);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (b ? kMxAcc1 : 0u);
+        for (int ks = 0; ks < nk; ++ks, ++g) {
+          const int s = g % kStages;
+          // this set of scale columns was read by the MMAs of stage g - 2
+          if (!mbar_wait(full(s), (uint32_t)(g / kStages) & 1u) ||
+              (g >= 2 && !mbar_wait(empty((g - 2) % kStages), (uint32_t)((g - 2) / kStages) & 1u))) {
+            mx_timeout(ctrl, 43);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sf = tmem + kMxSf + 24u * (g & 1);
+          const uint64_t dsf = plain_desc(st_sf(s));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            tc_cp_scales(sf + 4u * j, dsf + (uint64_t)((512 * j) >> 4));
+#pragma unroll
+            for (int r = 0; r < S::kRowBlocks; ++r)
+              tc_cp_scales(sf + 8u + 8u * j + 4u * r,
+                           dsf + (uint64_t)((S::kSfA + 512 * (j * S::kRowBlocks + r)) >> 4));
+          }
+          const uint64_t da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
+          const int steps = min(4, (args.K - ks * kMxStageK) / 64);
+          for (int q = 0; q < steps; ++q)
+            tc_mma_mxf4(d, da + (uint64_t)((32 * q) >> 4), db + (uint64_t)((32 * q) >> 4), (q & 1) ? id2 : id0,
+                        sf + 4u * (q >> 1), sf + 8u + 8u * (q >> 1), (ks | q) ? 1u : 0u);
+          tc_commit(empty(s));
+        }
+        if (ok) tc_commit(acc_full(b));
+      }
+      // after a give-up: what was issued is complete before the columns are freed
+      if (g > 0) (void)mbar_wait(empty((g - 1) % kStages), (uint32_t)((g - 1) / kStages) & 1u);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+    for (int tl = 0; tl < n_my; ++tl) {
+      const MxTile t = tile_at(tl);
+      const int b = tl & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_full(b), ((uint32_t)tl >> 1) & 1u))) {
+        if (lane == 0) mx_timeout(ctrl, 44);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + lane_base + (b ? kMxAcc1 : 0u);
+      const int r = 32 * q + lane;
+      uint8_t *op = static_cast<uint8_t *>(args.out) + ((size_t)(t.row0 + r) * args.N + t.n0) * 2;
+      // 16 features at a time, from the end that the other accumulator shares: its 48 columns come first
+      for (int i = 0; i < kFeat / 16; ++i) {
+        const int f = 16 * (b ? i : kFeat / 16 - 1 - i);
+        uint32_t v[16], u[16];
+        mx_ld16(acc + f, v);
+        if (UP) mx_ld16(acc + kFeat + f, u);
+        tmem_ld_wait16(v);
+        if (UP) tmem_ld_wait16(u);
+        if (NC > (int)kMxAcc1 && i == 2) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_over);
+        }
+        if (r < t.rows && t.n0 + f < args.N) {
+          float y[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            y[j] = __uint_as_float(v[j]);
+            if (UP) y[j] = __fdividef(y[j], 1.0f + expf(-y[j])) * __uint_as_float(u[j]);
+          }
+          store8(op, args.out_type, f, y);
+          store8(op, args.out_type, f + 8, y + 8);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty(b));
+    }
+    // rows behind the last group
+    const int kept = args.offsets ? mx_group(args, args.E - 1).y : args.n_rows;
+    const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const size_t n8 = (size_t)args.n_rows * (args.N / 8);
+    for (size_t i = (size_t)kept * (args.N / 8) + blockIdx.x * 128 + (tid - 128); i < n8; i += (size_t)G * 128)
+      store8(args.out, args.out_type, 8 * i, z);
+  } else if (warp >= 8) {
+    // ------------------------------------------------ scales: a thread one row of A and up to two of B
+    const int th = tid - 256, pitch = args.K / 32, last_w = args.E * args.N - 1;
+    const bool wide = args.K % 256 == 0;  // eight aligned bytes a row and stage
+    constexpr int kRowsB = NC == 256 ? 2 : 1;
+    int ltl = 0, lks = 0;  // the next stage to fetch
+    const uint8_t *pa = nullptr, *pb[kRowsB] = {};
+    auto fetch8 = [&](const uint8_t *p, int ks) {
+      if (wide) return __ldg(reinterpret_cast<const uint2 *>(p) + ks);
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // K % 64 == 0: whole pairs of scales
+        h[j] = 8 * ks + 2 * j < pitch ? __ldg(reinterpret_cast<const uint16_t *>(p) + 4 * ks + j) : 0x7f7fu;
+      return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    };
+    auto fetch = [&](uint2 v[1 + kRowsB]) {
+      if (ltl >= n_my) return;
+      if (lks == 0) {
+        const MxTile t = tile_at(ltl);
+        pa = args.a_scales + (size_t)(t.row0 + min(th, t.rows - 1)) * pitch;
+#pragma unroll
+        for (int j = 0; j < kRowsB; ++j) {
+          const int r = min(th + 128 * j, NC - 1);
+          const bool up = UP && r >= kFeat;
+          const int wr = min(t.group * args.N + t.n0 + (up ? r - kFeat : r), last_w);
+          pb[j] = (up ? args.up_scales : args.w_scales) + (size_t)wr * pitch;
+        }
+      }
+      v[0] = fetch8(pa, lks);
+#pragma unroll
+      for (int j = 0; j < kRowsB; ++j) v[1 + j] = fetch8(pb[j], lks);
+      if (++lks == nk) {
+        lks = 0;
+        ++ltl;
+      }
+    };
+    const int total_g = n_my * nk;
+    const uint32_t at = (uint32_t)(th & 31) * 16 + (uint32_t)(th >> 5) * 4;
+    uint2 v[2][1 + kRowsB];
+    fetch(v[0]);
+    fetch(v[1]);
+    bool ok = true;
+    for (int g0 = 0; g0 < total_g && ok; g0 += 2) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int g = g0 + p, s = g % kStages;
+        if (g >= total_g) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
+          if (lane == 0) mx_timeout(ctrl, 45);
+          ok = false;
+          break;
+        }
+        uint8_t *sf = gbase + (st_sf(s) - base) + at;
+        *reinterpret_cast<uint32_t *>(sf) = v[p][0].x;
+        *reinterpret_cast<uint32_t *>(sf + 512) = v[p][0].y;
+#pragma unroll
+        for (int j = 0; j < kRowsB; ++j) {
+          if (NC < 128 && th >= NC) continue;
+          *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * j) = v[p][1 + j].x;
+          *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * (S::kRowBlocks + j)) = v[p][1 + j].y;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(s));
+        fetch(v[p]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int NC, bool UP>
+cudaError_t launch_nc(const Mx4ProductArgs &p, cudaStream_t s) {
+  constexpr int kFeat = UP ? NC / 2 : NC;
+  const uint64_t kb = (uint64_t)p.K / 2, wr = (uint64_t)p.E * p.N;
+  CUtensorMap ta, tw, tu;
+  auto map = [&](CUtensorMap *m, const uint8_t *ptr, uint64_t rows, int box) {
+    return encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, kb, rows, kMxRowBytes, box,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!map(&ta, p.a_codes, p.n_rows, kMxBoxRows) || !map(&tw, p.w_codes, wr, kFeat) ||
+      !map(&tu, UP ? p.up_codes : p.w_codes, wr, kFeat))
+    return cudaErrorInvalidValue;
+  const int nt = (p.N + kFeat - 1) / kFeat;
+  const MxArgs a{p.offsets, p.a_scales, p.w_scales, p.up_scales, p.out, p.out_type, p.n_rows, p.K, p.N, p.E, nt, p.ctrl};
+  const int live = p.E < p.n_rows ? p.E : p.n_rows;  // at most: every live group's last tile is partial
+  const long long most = ((long long)p.n_rows / kMxRows + live) * nt;
+  const int grid = (int)(most < num_sms() ? most : num_sms());
+  const cudaError_t e = smem_limit_once(mx4_product_kernel<NC, UP>, MxSmem<NC>::bytes(kMaxE));
+  if (e != cudaSuccess) return e;
+  KTimer kt_(KID_MX4_PRODUCT, s);
+  mx4_product_kernel<NC, UP><<<grid, kMxThreads, MxSmem<NC>::bytes(p.E), s>>>(ta, tw, tu, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_product(const Mx4ProductArgs &p, cudaStream_t s) {
+  // columns of a tile: as many as leave four tiles an SM, so that the last round's idle SMs cost little
+  const bool up = p.up_codes != nullptr;
+  const int live = p.E < p.n_rows ? p.E : p.n_rows;
+  auto tiles = [&](int nc) {
+    const int feat = up ? nc / 2 : nc;
+    return ((long long)p.n_rows / kMxRows + live) * ((p.N + feat - 1) / feat);
+  };
+  const long long want = 4ll * num_sms();
+  if (tiles(256) >= want) return up ? launch_nc<256, true>(p, s) : launch_nc<256, false>(p, s);
+  if (tiles(128) >= want) return up ? launch_nc<128, true>(p, s) : launch_nc<128, false>(p, s);
+  return up ? launch_nc<64, true>(p, s) : launch_nc<64, false>(p, s);
+}
+
+}  // namespace moe
