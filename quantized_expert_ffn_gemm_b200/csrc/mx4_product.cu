@@ -31,6 +31,7 @@ constexpr int kMxRows = 128;     // rows of a tile
 constexpr int kMxBoxRows = 32;   // rows of one TMA box of A: a short tile loads only the boxes it has rows in
 constexpr int kMxStageK = 256;   // K of a stage
 constexpr int kMxRowBytes = kMxStageK / 2;
+constexpr int kMxTileCache = 128;  // tiles whose place is worked out once, in the prologue
 constexpr uint32_t kMxAcc1 = 208;  // column of the second accumulator
 constexpr uint32_t kMxSf = 464;    // columns of the scales: two sets of 24
 
@@ -43,7 +44,8 @@ struct MxSmem {
   static constexpr int kStages = NC == 256 ? 4 : NC == 128 ? 5 : 7;
   static constexpr int kBar = kStages * kStage;
   static constexpr int kNumBars = 2 * kStages + 5;
-  static constexpr int kPrefix = kBar + (kNumBars * 8 + 16 + 15) / 16 * 16;
+  static constexpr int kTiles = kBar + (kNumBars * 8 + 16 + 15) / 16 * 16;
+  static constexpr int kPrefix = kTiles + kMxTileCache * 16;
   static constexpr int bytes(int E) { return kPrefix + (E + 1) * 4 + 1024; }
   static_assert(kStage % 1024 == 0, "stages start on swizzle atoms");
 };
@@ -56,7 +58,7 @@ struct MxArgs {
   Ctrl *ctrl;
 };
 
-struct MxTile {
+struct alignas(16) MxTile {
   int group, row0, rows, n0;
 };
 
@@ -90,6 +92,15 @@ __device__ __forceinline__ void mx_ld16(uint32_t taddr, uint32_t r[16]) {
       : "memory");
 }
 
+// one lane of a converged warp. The TMA and MMA warps run their loops with all lanes and issue from the
+// elected one: addresses and descriptors are then the same in every lane and stay in uniform
+// registers. Loops run by lane 0 alone took 180 cycles an MMA instead of its 128.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void mx_timeout(Ctrl *ctrl, int where) { set_device_error(ctrl, MOE_ERR_TIMEOUT, where); }
 
 // start and end row of a group, whatever the offsets hold: 0 <= start <= end <= n_rows
@@ -98,6 +109,92 @@ __device__ __forceinline__ int2 mx_group(const MxArgs &a, int g) {
   const int s = min(max(__ldg(a.offsets + g), 0), a.n_rows);
   return make_int2(s, min(max(__ldg(a.offsets + g + 1), s), a.n_rows));
 }
+
+// The scale bytes of one thread's rows, fetched kAhead chunks before they are put into their stage: the
+// loads come from HBM for a group's first row tile, and a stage lasts 0.3-0.5 us, so two stages ahead
+// (measured first) left the MMAs waiting for them. A chunk is C stages: 16 bytes a row where the
+// row pitch allows, 8 otherwise.
+template <int NC, bool UP, class TileAt>
+struct MxScales {
+  static constexpr int kRows = 1 + MxSmem<NC>::kRowBlocks, kFeat = UP ? NC / 2 : NC, kAhead = 4;
+  const MxArgs &a;
+  const TileAt &tile_at;
+  const int n_my, nk, th;
+  int tl = 0, ks = 0;  // the next chunk to fetch
+  const uint8_t *p[kRows] = {};
+
+  __device__ __forceinline__ void stage8(const uint8_t *q, uint32_t v[2]) const {
+    const int pitch = a.K / 32;
+    if (a.K % 256 == 0) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q) + ks);
+      v[0] = w.x;
+      v[1] = w.y;
+      return;
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // K % 64 == 0: whole pairs of scales
+      h[j] = 8 * ks + 2 * j < pitch ? __ldg(reinterpret_cast<const uint16_t *>(q) + 4 * ks + j) : 0x7f7fu;
+    v[0] = h[0] | h[1] << 16;
+    v[1] = h[2] | h[3] << 16;
+  }
+
+  template <int C>
+  __device__ __forceinline__ void fetch(uint32_t v[kRows][2 * C]) {
+    if (tl >= n_my) return;
+    if (ks == 0) {
+      const MxTile t = tile_at(tl);
+      const int pitch = a.K / 32;
+      p[0] = a.a_scales + (size_t)(t.row0 + min(th, t.rows - 1)) * pitch;
+#pragma unroll
+      for (int j = 1; j < kRows; ++j) {
+        const int r = min(th + 128 * (j - 1), NC - 1);
+        const bool up = UP && r >= kFeat;
+        const int wr = min(t.group * a.N + t.n0 + (up ? r - kFeat : r), a.E * a.N - 1);
+        p[j] = (up ? a.up_scales : a.w_scales) + (size_t)wr * pitch;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if constexpr (C == 2) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p[j] + 8 * ks));
+        v[j][0] = w.x;
+        v[j][1] = w.y;
+        v[j][2] = w.z;
+        v[j][3] = w.w;
+      } else {
+        stage8(p[j], v[j]);
+      }
+    }
+    ks += C;
+    if (ks >= nk) {
+      ks = 0;
+      ++tl;
+    }
+  }
+
+  template <int C, class Put>
+  __device__ __forceinline__ void run(const Put &put) {
+    const int total = n_my * nk / C;  // C divides nk
+    uint32_t v[kAhead][kRows][2 * C];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) fetch<C>(v[j]);
+    for (int c0 = 0; c0 < total; c0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (c0 + j >= total) return;
+#pragma unroll
+        for (int h = 0; h < C; ++h) {
+          uint2 w[kRows];
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) w[r] = make_uint2(v[j][r][2 * h], v[j][r][2 * h + 1]);
+          if (!put((c0 + j) * C + h, w)) return;
+        }
+        fetch<C>(v[j]);
+      }
+    }
+  }
+};
 
 template <int NC, bool UP>
 __global__ void __launch_bounds__(kMxThreads, 1)
@@ -120,7 +217,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   int32_t *s_pref = reinterpret_cast<int32_t *>(gbase + S::kPrefix);  // [E + 1] tiles before a group
   __shared__ int32_t s_warp[kMxThreads / 32];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   Ctrl *ctrl = args.ctrl;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -168,11 +265,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int total = s_pref[args.E], G = gridDim.x, nk = (args.K + kMxStageK - 1) / kMxStageK;
   const int n_my = total > (int)blockIdx.x ? (total - (int)blockIdx.x + G - 1) / G : 0;
 
-  auto tile_at = [&](int tl) {
+  auto find_tile = [&](int tl) {
     const int ti = blockIdx.x + tl * G;
     int lo = 0, hi = args.E - 1;  // the last group that starts at or before the tile and has one
     while (lo < hi) {
@@ -189,60 +286,75 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     t.n0 = (local / mt) * kFeat;
     return t;
   };
+  MxTile *s_tiles = reinterpret_cast<MxTile *>(gbase + S::kTiles);
+  if (tid < min(n_my, kMxTileCache)) s_tiles[tid] = find_tile(tid);
+  __syncthreads();
+  auto uniform_tile = [&](MxTile t) {
+    t.group = __shfl_sync(0xffffffffu, t.group, 0);
+    t.row0 = __shfl_sync(0xffffffffu, t.row0, 0);
+    t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+    t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+    return t;
+  };
+  auto tile_at = [&](int tl) { return tl < kMxTileCache ? s_tiles[tl] : find_tile(tl); };
 
   if (warp == 0) {
     // ------------------------------------------------ TMA
-    if (lane == 0) {
-      bool ok = true;
-      int g = 0;
-      for (int tl = 0; tl < n_my && ok; ++tl) {
-        const MxTile t = tile_at(tl);
-        const int nbox = (t.rows + kMxBoxRows - 1) / kMxBoxRows, wrow = t.group * args.N + t.n0;
-        const uint32_t tx = (uint32_t)(nbox * kMxBoxRows + NC) * kMxRowBytes;
-        for (int ks = 0; ks < nk; ++ks, ++g) {
-          const int s = g % kStages;
-          if (!mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u)) {
-            mx_timeout(ctrl, 41);
-            ok = false;
-            break;
-          }
+    bool ok = true;
+    int g = 0;
+    for (int tl = 0; tl < n_my && ok; ++tl) {
+      const MxTile t = uniform_tile(tile_at(tl));
+      const int nbox = (t.rows + kMxBoxRows - 1) / kMxBoxRows, wrow = t.group * args.N + t.n0;
+      const uint32_t tx = (uint32_t)(nbox * kMxBoxRows + NC) * kMxRowBytes;
+      for (int ks = 0; ks < nk; ++ks, ++g) {
+        const int s = g % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
+          if (lane == 0) mx_timeout(ctrl, 41);
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           mbar_arrive_expect_tx(full(s), tx);
-          for (int b = 0; b < nbox; ++b)
-            tma_load_2d(st_a(s) + b * kMxBoxRows * kMxRowBytes, &tm_a, ks * kMxRowBytes, t.row0 + b * kMxBoxRows, full(s));
           tma_load_2d(st_b(s), &tm_w, ks * kMxRowBytes, wrow, full(s));
           if (UP) tma_load_2d(st_b(s) + kFeat * kMxRowBytes, &tm_u, ks * kMxRowBytes, wrow, full(s));
+          for (int b = 0; b < nbox; ++b)
+            tma_load_2d(st_a(s) + b * kMxBoxRows * kMxRowBytes, &tm_a, ks * kMxRowBytes, t.row0 + b * kMxBoxRows, full(s));
         }
+        __syncwarp();
       }
-      // after a give-up somewhere: the copies of the last stages have landed before the CTA leaves
-      for (int j = max(0, g - kStages); j < g; ++j) (void)mbar_wait(full(j % kStages), (uint32_t)(j / kStages) & 1u);
     }
+    // after a give-up somewhere: the copies of the last stages have landed before the CTA leaves
+    for (int j = max(0, g - kStages); j < g; ++j) (void)mbar_wait(full(j % kStages), (uint32_t)(j / kStages) & 1u);
   } else if (warp == 1) {
     // ------------------------------------------------ MMA
-    if (lane == 0) {
-      const uint32_t id0 = idesc_mxf4(NC, 0), id2 = idesc_mxf4(NC, 2);
-      bool ok = true;
-      int g = 0;
-      for (int tl = 0; tl < n_my && ok; ++tl) {
-        const int b = tl & 1;
-        if (!mbar_wait(acc_empty(b), (((uint32_t)tl >> 1) & 1u) ^ 1u) ||
-            (NC > (int)kMxAcc1 && tl > 0 && !mbar_wait(acc_over, (uint32_t)(tl - 1) & 1u))) {
-          mx_timeout(ctrl, 42);
+    const uint32_t id0 = idesc_mxf4(NC, 0), id2 = idesc_mxf4(NC, 2);
+    bool ok = true;
+    int g = 0;
+    for (int tl = 0; tl < n_my && ok; ++tl) {
+      const int b = tl & 1;
+      const bool go = mbar_wait(acc_empty(b), (((uint32_t)tl >> 1) & 1u) ^ 1u) &&
+                      (NC <= (int)kMxAcc1 || tl == 0 || mbar_wait(acc_over, (uint32_t)(tl - 1) & 1u));
+      if (!__all_sync(0xffffffffu, go)) {
+        if (lane == 0) mx_timeout(ctrl, 42);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + (b ? kMxAcc1 : 0u);
+      for (int ks = 0; ks < nk; ++ks, ++g) {
+        const int s = g % kStages;
+        // this set of scale columns was read by the MMAs of stage g - 2
+        const bool in = mbar_wait(full(s), (uint32_t)(g / kStages) & 1u) &&
+                        (g < 2 || mbar_wait(empty((g - 2) % kStages), (uint32_t)((g - 2) / kStages) & 1u));
+        if (!__all_sync(0xffffffffu, in)) {
+          if (lane == 0) mx_timeout(ctrl, 43);
+          ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (b ? kMxAcc1 : 0u);
-        for (int ks = 0; ks < nk; ++ks, ++g) {
-          const int s = g % kStages;
-          // this set of scale columns was read by the MMAs of stage g - 2
-          if (!mbar_wait(full(s), (uint32_t)(g / kStages) & 1u) ||
-              (g >= 2 && !mbar_wait(empty((g - 2) % kStages), (uint32_t)((g - 2) / kStages) & 1u))) {
-            mx_timeout(ctrl, 43);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sf = tmem + kMxSf + 24u * (g & 1);
-          const uint64_t dsf = plain_desc(st_sf(s));
+        const uint32_t sf = tmem + kMxSf + 24u * (g & 1);
+        const uint64_t dsf = plain_desc(st_sf(s)), da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
+        const int steps = (args.K - ks * kMxStageK) / 64;
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             tc_cp_scales(sf + 4u * j, dsf + (uint64_t)((512 * j) >> 4));
@@ -251,18 +363,19 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
               tc_cp_scales(sf + 8u + 8u * j + 4u * r,
                            dsf + (uint64_t)((S::kSfA + 512 * (j * S::kRowBlocks + r)) >> 4));
           }
-          const uint64_t da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
-          const int steps = min(4, (args.K - ks * kMxStageK) / 64);
-          for (int q = 0; q < steps; ++q)
-            tc_mma_mxf4(d, da + (uint64_t)((32 * q) >> 4), db + (uint64_t)((32 * q) >> 4), (q & 1) ? id2 : id0,
-                        sf + 4u * (q >> 1), sf + 8u + 8u * (q >> 1), (ks | q) ? 1u : 0u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < steps)
+              tc_mma_mxf4(d, da + (uint64_t)((32 * q) >> 4), db + (uint64_t)((32 * q) >> 4), (q & 1) ? id2 : id0,
+                          sf + 4u * (q >> 1), sf + 8u + 8u * (q >> 1), (ks | q) ? 1u : 0u);
           tc_commit(empty(s));
+          if (ks == nk - 1) tc_commit(acc_full(b));
         }
-        if (ok) tc_commit(acc_full(b));
+        __syncwarp();
       }
-      // after a give-up: what was issued is complete before the columns are freed
-      if (g > 0) (void)mbar_wait(empty((g - 1) % kStages), (uint32_t)((g - 1) / kStages) & 1u);
     }
+    // after a give-up: what was issued is complete before the columns are freed
+    if (g > 0) (void)mbar_wait(empty((g - 1) % kStages), (uint32_t)((g - 1) / kStages) & 1u);
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------ epilogue
     const int q = warp & 3;
@@ -314,71 +427,29 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       store8(args.out, args.out_type, 8 * i, z);
   } else if (warp >= 8) {
     // ------------------------------------------------ scales: a thread one row of A and up to two of B
-    const int th = tid - 256, pitch = args.K / 32, last_w = args.E * args.N - 1;
-    const bool wide = args.K % 256 == 0;  // eight aligned bytes a row and stage
-    constexpr int kRowsB = NC == 256 ? 2 : 1;
-    int ltl = 0, lks = 0;  // the next stage to fetch
-    const uint8_t *pa = nullptr, *pb[kRowsB] = {};
-    auto fetch8 = [&](const uint8_t *p, int ks) {
-      if (wide) return __ldg(reinterpret_cast<const uint2 *>(p) + ks);
-      uint32_t h[4];
+    MxScales<NC, UP, decltype(tile_at)> w{args, tile_at, n_my, nk, tid - 256};
+    auto put = [&](int g, const uint2 v[]) {  // a stage's eight bytes of each of this thread's rows
+      const int s = g % kStages, th = tid - 256;
+      if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
+        if (lane == 0) mx_timeout(ctrl, 45);
+        return false;
+      }
+      uint8_t *sf = gbase + (st_sf(s) - base) + (th & 31) * 16 + (th >> 5) * 4;
+      *reinterpret_cast<uint32_t *>(sf) = v[0].x;
+      *reinterpret_cast<uint32_t *>(sf + 512) = v[0].y;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)  // K % 64 == 0: whole pairs of scales
-        h[j] = 8 * ks + 2 * j < pitch ? __ldg(reinterpret_cast<const uint16_t *>(p) + 4 * ks + j) : 0x7f7fu;
-      return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+      for (int j = 0; j < S::kRowBlocks; ++j) {
+        if (NC < 128 && th >= NC) continue;
+        *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * j) = v[1 + j].x;
+        *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * (S::kRowBlocks + j)) = v[1 + j].y;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(s));
+      return true;
     };
-    auto fetch = [&](uint2 v[1 + kRowsB]) {
-      if (ltl >= n_my) return;
-      if (lks == 0) {
-        const MxTile t = tile_at(ltl);
-        pa = args.a_scales + (size_t)(t.row0 + min(th, t.rows - 1)) * pitch;
-#pragma unroll
-        for (int j = 0; j < kRowsB; ++j) {
-          const int r = min(th + 128 * j, NC - 1);
-          const bool up = UP && r >= kFeat;
-          const int wr = min(t.group * args.N + t.n0 + (up ? r - kFeat : r), last_w);
-          pb[j] = (up ? args.up_scales : args.w_scales) + (size_t)wr * pitch;
-        }
-      }
-      v[0] = fetch8(pa, lks);
-#pragma unroll
-      for (int j = 0; j < kRowsB; ++j) v[1 + j] = fetch8(pb[j], lks);
-      if (++lks == nk) {
-        lks = 0;
-        ++ltl;
-      }
-    };
-    const int total_g = n_my * nk;
-    const uint32_t at = (uint32_t)(th & 31) * 16 + (uint32_t)(th >> 5) * 4;
-    uint2 v[2][1 + kRowsB];
-    fetch(v[0]);
-    fetch(v[1]);
-    bool ok = true;
-    for (int g0 = 0; g0 < total_g && ok; g0 += 2) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int g = g0 + p, s = g % kStages;
-        if (g >= total_g) break;
-        if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
-          if (lane == 0) mx_timeout(ctrl, 45);
-          ok = false;
-          break;
-        }
-        uint8_t *sf = gbase + (st_sf(s) - base) + at;
-        *reinterpret_cast<uint32_t *>(sf) = v[p][0].x;
-        *reinterpret_cast<uint32_t *>(sf + 512) = v[p][0].y;
-#pragma unroll
-        for (int j = 0; j < kRowsB; ++j) {
-          if (NC < 128 && th >= NC) continue;
-          *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * j) = v[p][1 + j].x;
-          *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * (S::kRowBlocks + j)) = v[p][1 + j].y;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(s));
-        fetch(v[p]);
-      }
-    }
+    if (args.K % 512 == 0) w.template run<2>(put);
+    else w.template run<1>(put);
   }
   tc_fence_before();
   __syncthreads();
