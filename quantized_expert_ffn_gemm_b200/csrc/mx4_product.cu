@@ -12,10 +12,13 @@
 //   stage   K = 256: 128 bytes of codes a row (one 128-byte swizzle row), four MMAs of K = 64
 //   scales  per 128 rows and K = 128 one 512-byte block, row r's four bytes at (r % 32) 16 + (r / 32) 4;
 //           tcgen05.cp puts it into 4 columns of all four lane quarters. An MMA reads bytes 0-1 or 2-3.
-//   TMEM    two accumulators of NC columns and two sets of a stage's scales. NC = 256 leaves 48 columns
-//           for the scales if the accumulators (columns 0 and 208) share 48: a tile's epilogue
-//           reads the shared ones first and then lets the next tile begin.
-//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warps 4-7 epilogue, warps 8-11 scales.
+//   TMEM    two accumulators of NC columns and a set of scale columns a stage in flight. With NC = 256 the
+//           accumulators (columns 0 and 176) share 80 columns, which leaves room for three sets: a
+//           tile's epilogue reads the shared ones first and then lets the next tile begin. (Two sets
+//           held each stage until the one but last had finished: about 1000 cycles from a stage's
+//           issue to its commit, 555 a stage of an NC = 64 tile, whose MMAs take 128.)
+//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warps 4-11 epilogue (two a lane quarter),
+//           warps 12-15 scales.
 //
 // Tiles are dealt round-robin with a group's row tiles innermost, so a weight tile is read from HBM once and
 // by the group's other row tiles from L2. Every wait is bounded and reports MOE_ERR_TIMEOUT.
@@ -26,14 +29,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kMxThreads = 384;
+constexpr int kMxThreads = 512;
 constexpr int kMxRows = 128;     // rows of a tile
 constexpr int kMxBoxRows = 32;   // rows of one TMA box of A: a short tile loads only the boxes it has rows in
 constexpr int kMxStageK = 256;   // K of a stage
 constexpr int kMxRowBytes = kMxStageK / 2;
 constexpr int kMxTileCache = 128;  // tiles whose place is worked out once, in the prologue
-constexpr uint32_t kMxAcc1 = 208;  // column of the second accumulator
-constexpr uint32_t kMxSf = 464;    // columns of the scales: two sets of 24
 
 template <int NC>
 struct MxSmem {
@@ -42,6 +43,11 @@ struct MxSmem {
   static constexpr int kSfA = 2 * 512, kSfB = 2 * kRowBlocks * 512;  // two K = 128 blocks a stage
   static constexpr int kStage = kA + kB + kSfA + kSfB;
   static constexpr int kStages = NC == 256 ? 4 : NC == 128 ? 5 : 7;
+  // tensor memory: column of the second accumulator, of the scales, columns and number of the scale sets
+  static constexpr int kAcc1 = NC == 256 ? 176 : NC, kSf = kAcc1 + NC, kSfCols = 8 + 8 * kRowBlocks;
+  static constexpr int kSfSets = NC == 256 ? 3 : kStages;
+  static constexpr int kOver = NC - kAcc1;  // columns that both accumulators use
+  static_assert(kSf + kSfSets * kSfCols <= 512 && kOver % 16 == 0, "tensor memory");
   static constexpr int kBar = kStages * kStage;
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kTiles = kBar + (kNumBars * 8 + 16 + 15) / 16 * 16;
@@ -226,9 +232,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4);
+      mbar_init(acc_empty(b), 8);
     }
-    mbar_init(acc_over, 4);
+    mbar_init(acc_over, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -333,25 +339,28 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     for (int tl = 0; tl < n_my && ok; ++tl) {
       const int b = tl & 1;
       const bool go = mbar_wait(acc_empty(b), (((uint32_t)tl >> 1) & 1u) ^ 1u) &&
-                      (NC <= (int)kMxAcc1 || tl == 0 || mbar_wait(acc_over, (uint32_t)(tl - 1) & 1u));
+                      (S::kOver == 0 || tl == 0 || mbar_wait(acc_over, (uint32_t)(tl - 1) & 1u));
       if (!__all_sync(0xffffffffu, go)) {
         if (lane == 0) mx_timeout(ctrl, 42);
         break;
       }
       tc_fence_after();
-      const uint32_t d = tmem + (b ? kMxAcc1 : 0u);
+      const uint32_t d = tmem + (uint32_t)(b * S::kAcc1);
       for (int ks = 0; ks < nk; ++ks, ++g) {
         const int s = g % kStages;
-        // this set of scale columns was read by the MMAs of stage g - 2
+        // the scale columns of stage g were read by the MMAs of stage g - kSfSets; with a set a stage
+        // the stage's own slot says so
+        constexpr int kBack = S::kSfSets;
         const bool in = mbar_wait(full(s), (uint32_t)(g / kStages) & 1u) &&
-                        (g < 2 || mbar_wait(empty((g - 2) % kStages), (uint32_t)((g - 2) / kStages) & 1u));
+                        (kBack == kStages || g < kBack ||
+                         mbar_wait(empty((g - kBack) % kStages), (uint32_t)((g - kBack) / kStages) & 1u));
         if (!__all_sync(0xffffffffu, in)) {
           if (lane == 0) mx_timeout(ctrl, 43);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sf = tmem + kMxSf + 24u * (g & 1);
+        const uint32_t sf = tmem + (uint32_t)(S::kSf + g % kBack * S::kSfCols);
         const uint64_t dsf = plain_desc(st_sf(s)), da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
         const int steps = (args.K - ks * kMxStageK) / 64;
         if (elect_one()) {
@@ -376,10 +385,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     }
     // after a give-up: what was issued is complete before the columns are freed
     if (g > 0) (void)mbar_wait(empty((g - 1) % kStages), (uint32_t)((g - 1) / kStages) & 1u);
-  } else if (warp >= 4 && warp < 8) {
-    // ------------------------------------------------ epilogue
-    const int q = warp & 3;
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------ epilogue: a lane quarter and every other 16 features
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+    constexpr int kChunks = kFeat / 16, kIt = kFeat / 32;
+    const int over_it = (S::kOver / 16 - 1 - half) / 2;  // this warp's last chunk of shared columns
     for (int tl = 0; tl < n_my; ++tl) {
       const MxTile t = tile_at(tl);
       const int b = tl & 1;
@@ -388,31 +399,46 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         break;
       }
       tc_fence_after();
-      const uint32_t acc = tmem + lane_base + (b ? kMxAcc1 : 0u);
+      const uint32_t acc = tmem + lane_base + (uint32_t)(b * S::kAcc1);
       const int r = 32 * q + lane;
       uint8_t *op = static_cast<uint8_t *>(args.out) + ((size_t)(t.row0 + r) * args.N + t.n0) * 2;
-      // 16 features at a time, from the end that the other accumulator shares: its 48 columns come first
-      for (int i = 0; i < kFeat / 16; ++i) {
-        const int f = 16 * (b ? i : kFeat / 16 - 1 - i);
-        uint32_t v[16], u[16];
-        mx_ld16(acc + f, v);
-        if (UP) mx_ld16(acc + kFeat + f, u);
-        tmem_ld_wait16(v);
-        if (UP) tmem_ld_wait16(u);
-        if (NC > (int)kMxAcc1 && i == 2) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_over);
-        }
-        if (r < t.rows && t.n0 + f < args.N) {
-          float y[16];
+      // from the end that the other accumulator shares, so that those columns are read first
+      auto feat = [&](int it) { return 16 * (b ? 2 * it + half : kChunks - 1 - 2 * it - half); };
+      uint32_t v[2][16], u[2][16];
+      auto load = [&](int it, int p) {
+        mx_ld16(acc + feat(it), v[p]);
+        if (UP) mx_ld16(acc + kFeat + feat(it), u[p]);
+      };
+      const bool any = 32 * q < t.rows;  // a quarter without rows has nothing to read
+      if (any) load(0, 0);
+#pragma unroll 1
+      for (int it0 = 0; it0 < kIt; it0 += 2) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            y[j] = __uint_as_float(v[j]);
-            if (UP) y[j] = __fdividef(y[j], 1.0f + expf(-y[j])) * __uint_as_float(u[j]);
+        for (int p = 0; p < 2; ++p) {
+          const int it = it0 + p;
+          if (it >= kIt) break;
+          if (any) {
+            tmem_ld_wait16(v[p]);
+            if (UP) tmem_ld_wait16(u[p]);
           }
-          store8(op, args.out_type, f, y);
-          store8(op, args.out_type, f + 8, y + 8);
+          if (S::kOver && it == over_it) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_over);
+          }
+          if (!any) continue;
+          if (it + 1 < kIt) load(it + 1, p ^ 1);
+          const int f = feat(it);
+          if (r < t.rows && t.n0 + f < args.N) {
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              y[j] = __uint_as_float(v[p][j]);
+              if (UP) y[j] = __fdividef(y[j], 1.0f + __expf(-y[j])) * __uint_as_float(u[p][j]);
+            }
+            store8(op, args.out_type, f, y);
+            store8(op, args.out_type, f + 8, y + 8);
+          }
         }
       }
       tc_fence_before();
@@ -423,13 +449,13 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int kept = args.offsets ? mx_group(args, args.E - 1).y : args.n_rows;
     const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const size_t n8 = (size_t)args.n_rows * (args.N / 8);
-    for (size_t i = (size_t)kept * (args.N / 8) + blockIdx.x * 128 + (tid - 128); i < n8; i += (size_t)G * 128)
+    for (size_t i = (size_t)kept * (args.N / 8) + blockIdx.x * 256 + (tid - 128); i < n8; i += (size_t)G * 256)
       store8(args.out, args.out_type, 8 * i, z);
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ------------------------------------------------ scales: a thread one row of A and up to two of B
-    MxScales<NC, UP, decltype(tile_at)> w{args, tile_at, n_my, nk, tid - 256};
+    MxScales<NC, UP, decltype(tile_at)> w{args, tile_at, n_my, nk, tid - 384};
     auto put = [&](int g, const uint2 v[]) {  // a stage's eight bytes of each of this thread's rows
-      const int s = g % kStages, th = tid - 256;
+      const int s = g % kStages, th = tid - 384;
       if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
         if (lane == 0) mx_timeout(ctrl, 45);
         return false;
