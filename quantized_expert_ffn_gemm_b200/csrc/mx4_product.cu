@@ -13,10 +13,12 @@
 //   scales  per 128 rows and K = 128 one 512-byte block, row r's four bytes at (r % 32) 16 + (r / 32) 4;
 //           tcgen05.cp puts it into 4 columns of all four lane quarters. An MMA reads bytes 0-1 or 2-3.
 //   TMEM    two accumulators of NC columns and a set of scale columns a stage in flight. With NC = 256 the
-//           accumulators (columns 0 and 176) share 80 columns, which leaves room for three sets: a
-//           tile's epilogue reads the shared ones first and then lets the next tile begin. (Two sets
-//           held each stage until the one but last had finished: about 1000 cycles from a stage's
-//           issue to its commit, 555 a stage of an NC = 64 tile, whose MMAs take 128.)
+//           accumulators (columns 0 and 208) share 48 columns, which leaves room for two sets: a
+//           tile's epilogue first reads the shared ones into registers and lets the next tile begin.
+//           (Two sets hold a stage until the one but last has finished, about 1000 cycles from issue to
+//           commit: no loss while a stage's MMAs take 512, but 555 cycles a stage of an NC = 64
+//           tile, whose MMAs take 128. Three sets and 80 shared columns: the next tile began
+//           2000 cycles after a tile's end instead of 600.)
 //   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warps 4-11 epilogue (two a lane quarter),
 //           warps 12-15 scales.
 //
@@ -44,8 +46,8 @@ struct MxSmem {
   static constexpr int kStage = kA + kB + kSfA + kSfB;
   static constexpr int kStages = NC == 256 ? 4 : NC == 128 ? 5 : 7;
   // tensor memory: column of the second accumulator, of the scales, columns and number of the scale sets
-  static constexpr int kAcc1 = NC == 256 ? 176 : NC, kSf = kAcc1 + NC, kSfCols = 8 + 8 * kRowBlocks;
-  static constexpr int kSfSets = NC == 256 ? 3 : kStages;
+  static constexpr int kAcc1 = NC == 256 ? 208 : NC, kSf = kAcc1 + NC, kSfCols = 8 + 8 * kRowBlocks;
+  static constexpr int kSfSets = NC == 256 ? 2 : kStages;
   static constexpr int kOver = NC - kAcc1;  // columns that both accumulators use
   static_assert(kSf + kSfSets * kSfCols <= 512 && kOver % 16 == 0, "tensor memory");
   static constexpr int kBar = kStages * kStage;
@@ -105,6 +107,27 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
   return p != 0;
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int type) {
+  if (type == MOE_BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// A lane's 32 bytes of its own row: a warp's store touches 32 lines whatever its width, and their number is
+// what the epilogue's stores cost, so one 32-byte store beats two of 16.
+__device__ __forceinline__ void store32(void *p, const uint32_t y[8], bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                 "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                 : "memory");
+    return;
+  }
+  static_cast<uint4 *>(p)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  static_cast<uint4 *>(p)[1] = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
 __device__ __forceinline__ void mx_timeout(Ctrl *ctrl, int where) { set_device_error(ctrl, MOE_ERR_TIMEOUT, where); }
@@ -390,7 +413,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     constexpr int kChunks = kFeat / 16, kIt = kFeat / 32;
-    const int over_it = (S::kOver / 16 - 1 - half) / 2;  // this warp's last chunk of shared columns
+    static_assert(S::kOver <= 48, "the shared columns are each warp's first chunk or two");
+    const bool out32 = ((uintptr_t)args.out & 31u) == 0;
     for (int tl = 0; tl < n_my; ++tl) {
       const MxTile t = tile_at(tl);
       const int b = tl & 1;
@@ -410,35 +434,44 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         if (UP) mx_ld16(acc + kFeat + feat(it), u[p]);
       };
       const bool any = 32 * q < t.rows;  // a quarter without rows has nothing to read
-      if (any) load(0, 0);
+      if (any) {
+        load(0, 0);
+        if (kIt > 1) load(1, 1);
+        tmem_ld_wait16(v[0]);
+        tmem_ld_wait16(v[1]);
+        if (UP) {
+          tmem_ld_wait16(u[0]);
+          tmem_ld_wait16(u[1]);
+        }
+      }
+      if (S::kOver) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_over);
+      }
 #pragma unroll 1
-      for (int it0 = 0; it0 < kIt; it0 += 2) {
+      for (int it0 = 0; any && it0 < kIt; it0 += 2) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const int it = it0 + p;
           if (it >= kIt) break;
-          if (any) {
+          const int f = feat(it);
+          if (it >= 2) {
             tmem_ld_wait16(v[p]);
             if (UP) tmem_ld_wait16(u[p]);
           }
-          if (S::kOver && it == over_it) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_over);
-          }
-          if (!any) continue;
-          if (it + 1 < kIt) load(it + 1, p ^ 1);
-          const int f = feat(it);
-          if (r < t.rows && t.n0 + f < args.N) {
-            float y[16];
+          uint32_t y[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              y[j] = __uint_as_float(v[p][j]);
-              if (UP) y[j] = __fdividef(y[j], 1.0f + __expf(-y[j])) * __uint_as_float(u[p][j]);
+          for (int j = 0; j < 8; ++j) {
+            float a = __uint_as_float(v[p][2 * j]), c = __uint_as_float(v[p][2 * j + 1]);
+            if (UP) {
+              a = __fdividef(a, 1.0f + __expf(-a)) * __uint_as_float(u[p][2 * j]);
+              c = __fdividef(c, 1.0f + __expf(-c)) * __uint_as_float(u[p][2 * j + 1]);
             }
-            store8(op, args.out_type, f, y);
-            store8(op, args.out_type, f + 8, y + 8);
+            y[j] = pack16(a, c, args.out_type);
           }
+          if (it + 2 < kIt) load(it + 2, p);
+          if (r < t.rows && t.n0 + f < args.N) store32(op + 2 * f, y, out32);
         }
       }
       tc_fence_before();
