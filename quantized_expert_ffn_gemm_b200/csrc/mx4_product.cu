@@ -20,7 +20,7 @@
 //           tile, whose MMAs take 128. Three sets and 80 shared columns: the next tile began
 //           2000 cycles after a tile's end instead of 600.)
 //   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warps 4-11 epilogue (two a lane quarter),
-//           warps 12-15 scales.
+//           warps 12 on scales.
 //
 // Tiles are dealt round-robin with a group's row tiles innermost, so a weight tile is read from HBM once and
 // by the group's other row tiles from L2. Every wait is bounded and reports MOE_ERR_TIMEOUT.
@@ -31,7 +31,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kMxThreads = 512;
 constexpr int kMxRows = 128;     // rows of a tile
 constexpr int kMxBoxRows = 32;   // rows of one TMA box of A: a short tile loads only the boxes it has rows in
 constexpr int kMxStageK = 256;   // K of a stage
@@ -44,7 +43,8 @@ struct MxSmem {
   static constexpr int kRowBlocks = (NC + 127) / 128;               // 128-row scale blocks of B
   static constexpr int kSfA = 2 * 512, kSfB = 2 * kRowBlocks * 512;  // two K = 128 blocks a stage
   static constexpr int kStage = kA + kB + kSfA + kSfB;
-  static constexpr int kStages = NC == 256 ? 4 : NC == 128 ? 5 : 7;
+  static constexpr int kStages = NC == 256 ? 4 : 6;
+  static constexpr int kScaleWarps = kStages / 2, kThreads = 32 * (12 + kScaleWarps);
   // tensor memory: column of the second accumulator, of the scales, columns and number of the scale sets
   static constexpr int kAcc1 = NC == 256 ? 208 : NC, kSf = kAcc1 + NC, kSfCols = 8 + 8 * kRowBlocks;
   static constexpr int kSfSets = NC == 256 ? 2 : kStages;
@@ -139,20 +139,30 @@ __device__ __forceinline__ int2 mx_group(const MxArgs &a, int g) {
   return make_int2(s, min(max(__ldg(a.offsets + g + 1), s), a.n_rows));
 }
 
-// The scale bytes of one thread's rows, fetched kAhead chunks before they are put into their stage: the
-// loads come from HBM for a group's first row tile, and a stage lasts 0.3-0.5 us, so two stages ahead
-// (measured first) left the MMAs waiting for them. A chunk is C stages: 16 bytes a row where the
-// row pitch allows, 8 otherwise.
+// The scale bytes of the stages whose slots one warp owns: it loads the scales of all rows (lane + 32 i) for a pair
+// of stages, waits for their slots, stores them and goes on to its slots' next pair, so that the loads
+// are as far ahead as the TMA's. (With every warp on every stage and four loads ahead in registers, the
+// oldest were waited for together with the youngest.) A warp sees every use of its slots in order: a
+// parity wait that skipped a use would take the phase before the last for the last. Where K % 512 = 0
+// a pair is 16 bytes a row, otherwise each stage's 8 are read apart. Four rows 32 apart are 16
+// consecutive bytes of a scale block.
 template <int NC, bool UP, class TileAt>
 struct MxScales {
-  static constexpr int kRows = 1 + MxSmem<NC>::kRowBlocks, kFeat = UP ? NC / 2 : NC, kAhead = 4;
+  static constexpr int kRows = 4 + NC / 32, kFeat = UP ? NC / 2 : NC;
   const MxArgs &a;
   const TileAt &tile_at;
-  const int n_my, nk, th;
-  int tl = 0, ks = 0;  // the next chunk to fetch
-  const uint8_t *p[kRows] = {};
+  const int n_my, nk, lane;
 
-  __device__ __forceinline__ void stage8(const uint8_t *q, uint32_t v[2]) const {
+  __device__ __forceinline__ const uint8_t *row(const MxTile &t, int i) const {
+    const int pitch = a.K / 32;
+    if (i < 4) return a.a_scales + (size_t)(t.row0 + min(lane + 32 * i, t.rows - 1)) * pitch;
+    const int r = lane + 32 * (i - 4);
+    const bool up = UP && r >= kFeat;
+    const int wr = min(t.group * a.N + t.n0 + (up ? r - kFeat : r), a.E * a.N - 1);
+    return (up ? a.up_scales : a.w_scales) + (size_t)wr * pitch;
+  }
+
+  __device__ __forceinline__ void load8(const uint8_t *q, int ks, uint32_t v[2]) const {
     const int pitch = a.K / 32;
     if (a.K % 256 == 0) {
       const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q) + ks);
@@ -168,65 +178,46 @@ struct MxScales {
     v[1] = h[2] | h[3] << 16;
   }
 
-  template <int C>
-  __device__ __forceinline__ void fetch(uint32_t v[kRows][2 * C]) {
-    if (tl >= n_my) return;
-    if (ks == 0) {
-      const MxTile t = tile_at(tl);
-      const int pitch = a.K / 32;
-      p[0] = a.a_scales + (size_t)(t.row0 + min(th, t.rows - 1)) * pitch;
+  // put(stage, words) stores a stage; false after a time-out
+  template <class Put>
+  __device__ __forceinline__ void run(int w, const Put &put) const {
+    const int total = n_my * nk;
+    const bool wide = a.K % 512 == 0;  // nk is even, a pair is in one tile
+    for (int g = 2 * w; g < total; g += MxSmem<NC>::kStages) {
+      uint32_t v[2][2][kRows];  // [stage][word]
+      const bool two = g + 1 < total;
+      if (wide) {
+        const MxTile t = tile_at(g / nk);
+        const int at = 8 * (g % nk);
 #pragma unroll
-      for (int j = 1; j < kRows; ++j) {
-        const int r = min(th + 128 * (j - 1), NC - 1);
-        const bool up = UP && r >= kFeat;
-        const int wr = min(t.group * a.N + t.n0 + (up ? r - kFeat : r), a.E * a.N - 1);
-        p[j] = (up ? a.up_scales : a.w_scales) + (size_t)wr * pitch;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      if constexpr (C == 2) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p[j] + 8 * ks));
-        v[j][0] = w.x;
-        v[j][1] = w.y;
-        v[j][2] = w.z;
-        v[j][3] = w.w;
-      } else {
-        stage8(p[j], v[j]);
-      }
-    }
-    ks += C;
-    if (ks >= nk) {
-      ks = 0;
-      ++tl;
-    }
-  }
-
-  template <int C, class Put>
-  __device__ __forceinline__ void run(const Put &put) {
-    const int total = n_my * nk / C;  // C divides nk
-    uint32_t v[kAhead][kRows][2 * C];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch<C>(v[j]);
-    for (int c0 = 0; c0 < total; c0 += kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (c0 + j >= total) return;
-#pragma unroll
-        for (int h = 0; h < C; ++h) {
-          uint2 w[kRows];
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) w[r] = make_uint2(v[j][r][2 * h], v[j][r][2 * h + 1]);
-          if (!put((c0 + j) * C + h, w)) return;
+        for (int i = 0; i < kRows; ++i) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row(t, i) + at));
+          v[0][0][i] = x.x;
+          v[0][1][i] = x.y;
+          v[1][0][i] = x.z;
+          v[1][1][i] = x.w;
         }
-        fetch<C>(v[j]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h && !two) break;
+          const MxTile t = tile_at((g + h) / nk);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            uint32_t x[2];
+            load8(row(t, i), (g + h) % nk, x);
+            v[h][0][i] = x[0];
+            v[h][1][i] = x[1];
+          }
+        }
       }
+      if (!put(g, v[0]) || (two && !put(g + 1, v[1]))) return;
     }
   }
 };
 
 template <int NC, bool UP>
-__global__ void __launch_bounds__(kMxThreads, 1)
+__global__ void __launch_bounds__(MxSmem<NC>::kThreads, 1)
 mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_u, const MxArgs args) {
   using S = MxSmem<NC>;
@@ -244,13 +235,13 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   const uint32_t acc_over = base + S::kBar + 8u * (2 * kStages + 4);  // the shared columns are read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + S::kBar + S::kNumBars * 8);
   int32_t *s_pref = reinterpret_cast<int32_t *>(gbase + S::kPrefix);  // [E + 1] tiles before a group
-  __shared__ int32_t s_warp[kMxThreads / 32];
+  __shared__ int32_t s_warp[S::kThreads / 32];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   Ctrl *ctrl = args.ctrl;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1 + 4);  // TMA's bytes, the scale warps
+      mbar_init(full(s), 2);  // TMA's bytes, the stage's scale warp
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -266,7 +257,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   {  // tiles before each group: every thread sums a run of groups, then a block scan of the runs
-    const int per = (args.E + kMxThreads - 1) / kMxThreads, g0 = tid * per, g1 = min(args.E, g0 + per);
+    const int per = (args.E + S::kThreads - 1) / S::kThreads, g0 = tid * per, g1 = min(args.E, g0 + per);
     int mine = 0;
     for (int g = g0; g < g1; ++g) {
       const int2 r = mx_group(args, g);
@@ -289,7 +280,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       s_pref[g] = run;
       run += (r.y - r.x + kMxRows - 1) / kMxRows * args.n_tiles_n;
     }
-    if (tid == kMxThreads - 1) s_pref[args.E] = run;
+    if (tid == S::kThreads - 1) s_pref[args.E] = run;
   }
   tc_fence_before();
   __syncthreads();
@@ -382,6 +373,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
           ok = false;
           break;
         }
+        // The scale warps wrote through the generic proxy, tcgen05.cp reads through the async one: the fence
+        // between them stands here, on the path from their arrival to the copy. In the scale warps it
+        // waited for their loads in flight as well, which undid the fetching ahead.
+        fence_async_smem();
         tc_fence_after();
         const uint32_t sf = tmem + (uint32_t)(S::kSf + g % kBack * S::kSfCols);
         const uint64_t dsf = plain_desc(st_sf(s)), da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
@@ -485,30 +480,32 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     for (size_t i = (size_t)kept * (args.N / 8) + blockIdx.x * 256 + (tid - 128); i < n8; i += (size_t)G * 256)
       store8(args.out, args.out_type, 8 * i, z);
   } else if (warp >= 12) {
-    // ------------------------------------------------ scales: a thread one row of A and up to two of B
-    MxScales<NC, UP, decltype(tile_at)> w{args, tile_at, n_my, nk, tid - 384};
-    auto put = [&](int g, const uint2 v[]) {  // a stage's eight bytes of each of this thread's rows
-      const int s = g % kStages, th = tid - 384;
+    // ------------------------------------------------ scales
+    const MxScales<NC, UP, decltype(tile_at)> scales{args, tile_at, n_my, nk, lane};
+    auto put = [&](int g, const uint32_t x[2][4 + NC / 32]) {  // stage g's scales of all rows
+      const int s = g % kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
         if (lane == 0) mx_timeout(ctrl, 45);
         return false;
       }
-      uint8_t *sf = gbase + (st_sf(s) - base) + (th & 31) * 16 + (th >> 5) * 4;
-      *reinterpret_cast<uint32_t *>(sf) = v[0].x;
-      *reinterpret_cast<uint32_t *>(sf + 512) = v[0].y;
+      uint4 *sf = reinterpret_cast<uint4 *>(gbase + (st_sf(s) - base)) + lane;
 #pragma unroll
-      for (int j = 0; j < S::kRowBlocks; ++j) {
-        if (NC < 128 && th >= NC) continue;
-        *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * j) = v[1 + j].x;
-        *reinterpret_cast<uint32_t *>(sf + S::kSfA + 512 * (S::kRowBlocks + j)) = v[1 + j].y;
+      for (int j = 0; j < 2; ++j) {
+        sf[32 * j] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+        uint4 *sb = sf + S::kSfA / 16 + 32 * j * S::kRowBlocks;
+        if constexpr (NC < 128) {
+          *reinterpret_cast<uint2 *>(sb) = make_uint2(x[j][4], x[j][5]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < S::kRowBlocks; ++r)
+            sb[32 * r] = make_uint4(x[j][4 + 4 * r], x[j][5 + 4 * r], x[j][6 + 4 * r], x[j][7 + 4 * r]);
+        }
       }
-      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(s));
       return true;
     };
-    if (args.K % 512 == 0) w.template run<2>(put);
-    else w.template run<1>(put);
+    scales.run(warp - 12, put);
   }
   tc_fence_before();
   __syncthreads();
@@ -538,7 +535,7 @@ cudaError_t launch_nc(const Mx4ProductArgs &p, cudaStream_t s) {
   const cudaError_t e = smem_limit_once(mx4_product_kernel<NC, UP>, MxSmem<NC>::bytes(kMaxE));
   if (e != cudaSuccess) return e;
   KTimer kt_(KID_MX4_PRODUCT, s);
-  mx4_product_kernel<NC, UP><<<grid, kMxThreads, MxSmem<NC>::bytes(p.E), s>>>(ta, tw, tu, a);
+  mx4_product_kernel<NC, UP><<<grid, MxSmem<NC>::kThreads, MxSmem<NC>::bytes(p.E), s>>>(ta, tw, tu, a);
   return cudaGetLastError();
 }
 

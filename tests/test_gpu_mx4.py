@@ -178,7 +178,7 @@ def test_product_on_a_stream_and_in_a_graph():
 
 
 @pytest.mark.parametrize("up", [False, True])
-@pytest.mark.parametrize("groups,K,N", [(80, 320, 1088), (80, 768, 576), (48, 512, 512), (48, 128, 704)])
+@pytest.mark.parametrize("groups,K,N", [(80, 2048, 576), (48, 2112, 320), (80, 320, 1088), (80, 768, 576), (48, 512, 512), (48, 128, 704)])
 def test_product_many_tiles(groups, K, N, up):
     """Several tiles a block, of every tile width, full and partial rows and columns."""
     check_product([(37 * i) % 200 for i in range(groups)], K, N, up, BF16)
