@@ -74,7 +74,7 @@ def lib():
         _lib.moe_workspace_bytes.argtypes = [ctypes.POINTER(LayerDesc), ctypes.c_int32]
         for name in EXPORTED[2:]:
             getattr(_lib, name).restype = ctypes.c_int32
-        _block.bind(_lib)
+        _block.bind(_lib, _raw_stream, MoeError)
         _lib.moe_kernel_name.restype = ctypes.c_char_p
         _lib.moe_kernel_name.argtypes = [ctypes.c_int32]
     return _lib
