@@ -6,7 +6,12 @@
 
 namespace moe {
 
-__host__ __device__ constexpr int type_bytes(int type) { return type == MOE_F32 ? 4 : 2; }
+// The kernels' type codes: the public ones, and fp32 whose base is 32-byte aligned, which moves eight values
+// in one access. Two 16-byte accesses 32 bytes apart between lanes touch each 32-byte sector twice.
+constexpr int kF32Wide = 3;
+inline int kernel_type(int type, const void *p) { return type == MOE_F32 && ((uintptr_t)p & 31u) == 0 ? kF32Wide : type; }
+__host__ __device__ constexpr bool is_f32(int type) { return type == MOE_F32 || type == kF32Wide; }
+__host__ __device__ constexpr int type_bytes(int type) { return is_f32(type) ? 4 : 2; }
 
 // eight consecutive values as loaded (16 or 32 bytes), so that several loads are in flight before any
 // is converted; `type` is the same for every thread of a launch
@@ -17,6 +22,13 @@ struct Raw8 {
 __device__ __forceinline__ Raw8 load_raw8(const void *base, int type, size_t i) {  // values i .. i+7, i % 8 == 0
   const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + i * type_bytes(type));
   Raw8 r;
+  if (type == kF32Wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+  }
   r.a = p[0];
   r.b = make_uint4(0, 0, 0, 0);
   if (type == MOE_F32) r.b = p[1];
@@ -25,7 +37,7 @@ __device__ __forceinline__ Raw8 load_raw8(const void *base, int type, size_t i) 
 
 __device__ __forceinline__ void raw8_to_float(const Raw8 &r, int type, float v[8]) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-  if (type == MOE_F32) {
+  if (is_f32(type)) {
     const uint32_t x[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -52,13 +64,39 @@ __device__ __forceinline__ void load8(const void *base, int type, size_t i, floa
   raw8_to_float(load_raw8(base, type, i), type, v);
 }
 
+__device__ __forceinline__ void store_raw8(void *base, int type, size_t i, const Raw8 &r) {
+  uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + i * type_bytes(type));
+  if (type == kF32Wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r.a.x), "r"(r.a.y), "r"(r.a.z),
+                 "r"(r.a.w), "r"(r.b.x), "r"(r.b.y), "r"(r.b.z), "r"(r.b.w)
+                 : "memory");
+    return;
+  }
+  p[0] = r.a;
+  if (type == MOE_F32) p[1] = r.b;
+}
+
+// The inner loops know types at compile time as far as it pays: eight fp32 values in one access, or a 16-bit
+// type (fp16 or bf16, told apart by a uniform branch), or any type (kAny). With every type told apart
+// at run time a row of the norm cost 58 instructions a value.
+constexpr int kAny = -1, k16 = 4;
+template <int KT>
+__device__ __forceinline__ int known_type(int type) {
+  if constexpr (KT == kF32Wide) return kF32Wide;
+  else if constexpr (KT == k16) return type == MOE_BF16 ? MOE_BF16 : MOE_F16;
+  else return type;
+}
+inline int known_of(int type) { return type == kF32Wide ? kF32Wide : type == MOE_F32 ? kAny : k16; }
+
 // the one rounding of a result: fp32 as it is, fp16 / bf16 to nearest even
 __device__ __forceinline__ void store8(void *base, int type, size_t i, const float v[8]) {
   uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + i * type_bytes(type));
   uint32_t w[4];
-  if (type == MOE_F32) {
-    p[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    p[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  if (is_f32(type)) {
+    Raw8 r;
+    r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    store_raw8(base, type, i, r);
     return;
   }
 #pragma unroll
@@ -84,6 +122,7 @@ struct BlockNormArgs {
   void *r_out, *u;  // either may be NULL
   int u_type;
   float *rstd_y, *rstd_u;  // either may be NULL
+  int r_out_type, gain_type;  // set by the launcher
 };
 cudaError_t launch_block_norm(const BlockNormArgs &a, cudaStream_t s);
 
@@ -97,6 +136,7 @@ struct BlockNormGradArgs {
   float res_scale;
   void *dr, *dy;  // dy NULL: no block output
   float *d_post_gain, *d_gate, *d_pre_gain;  // each may be NULL
+  int d_type, dr_type, dy_type, gain_type;  // set by the launcher
 };
 // partial sums over the rows of each CTA: [CTAs][2][H] fp32
 size_t block_norm_grad_scratch(int T, int H);

@@ -165,9 +165,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const void *__restrict__ 
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (c0 + 32 * c >= H8) continue;
-        uint4 *p = reinterpret_cast<uint4 *>(d + (size_t)(c0 + 32 * c) * 8 * es);
-        p[0] = v[c].a;
-        if (type == MOE_F32) p[1] = v[c].b;
+        store_raw8(d, type, (size_t)(c0 + 32 * c) * 8, v[c]);
       }
     }
   }

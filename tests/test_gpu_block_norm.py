@@ -143,6 +143,12 @@ def test_backward_types(r, y, u, gate):
     run_backward(dev(inputs(21, 448, r, y, u, gate)), 1.5)
 
 
+@pytest.mark.parametrize("y,u", [(F32, F32), (F32, BF16), (BF16, BF16)])
+def test_backward_longest_rows(y, u):
+    """Rows of up to 256 KB: through shared memory where they fit, else read again from memory."""
+    run_backward(dev(inputs(3, 16384, y=y, u=u)), 0.5)
+
+
 @pytest.mark.parametrize("H", [192, 4160])
 def test_backward_parts_left_out(H):
     c = dev(inputs(11, H, gate="token"))
