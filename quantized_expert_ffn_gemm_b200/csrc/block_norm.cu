@@ -182,9 +182,14 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(
   pdl_wait();
   struct Row {
     Raw8 r, u, d, y;
+    float su, sy, tok;  // the row's statistics and gate
   };
   auto fetch = [&](long long t, int i, Row &w) {
-    if (t >= a.T || i >= H8) return;
+    if (t >= a.T) return;
+    w.su = a.du ? a.rstd_u[t] : 0.0f;
+    w.sy = (a.y && a.post_norm) ? a.rstd_y[t] : 1.0f;
+    w.tok = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
+    if (i >= H8) return;
     const size_t at = (size_t)t * a.H + 8 * i;
     if (a.du) {
       w.r = load_raw8(a.r, rt, at);
@@ -198,13 +203,13 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(
   for (long long t = first; t - sub < a.T; t += stride) {  // every thread of the block stays for the sums
     const bool live = t < a.T;
     const size_t base = (size_t)t * a.H;
-    const float rstd_u = (a.du && live) ? a.rstd_u[t] : 0.0f;
-    const float rstd_y = (a.y && a.post_norm && live) ? a.rstd_y[t] : 1.0f;
-    const float tok = (a.gate_mode == MOE_GATE_TOKEN && live) ? a.gate[t] : 1.0f;
     if constexpr (kOne) {
       w = next;
       fetch(t + stride, lane, next);
+    } else {
+      fetch(t, H8, w);
     }
+    const float rstd_u = w.su, rstd_y = w.sy, tok = w.tok;
     // x = r' rstd_u and h = du pre_gain (u: du)
     float x[8], h[8], m_u = 0.0f;
     auto xh = [&](int i, float u[8]) {
