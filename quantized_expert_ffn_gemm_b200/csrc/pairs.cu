@@ -10,6 +10,8 @@
 // The sort is a stable counting sort: each block ranks a chunk of pairs (equal experts of a warp by
 // __match_any_sync, warps by a prefix over their counts), so the order is the same in every run.
 // Nothing here adds with atomics across blocks; sums run over j in order.
+#include <type_traits>
+
 #include "block.cuh"
 
 namespace moe {
@@ -173,9 +175,11 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const void *__restrict__ 
 }
 
 // one warp a (token, segment of 32 chunks), four rows' loads in flight
-__global__ void __launch_bounds__(256) collect_kernel(const void *__restrict__ rows, int type, int T, int k, int H,
+template <int KR, int KY>
+__global__ void __launch_bounds__(256) collect_kernel(const void *__restrict__ rows, int rows_type, int T, int k, int H,
                                                      const int32_t *__restrict__ row_of, const float *__restrict__ w,
-                                                     const float *residual, void *y, int y_type) {
+                                                     const float *residual, void *y, int out_type) {
+  const int type = known_type<KR>(rows_type), y_type = known_type<KY>(out_type);
   const int lane = threadIdx.x & 31, H8 = H >> 3, nseg = (H8 + 31) >> 5, P = T * k;
   const long long n_items = (long long)T * nseg, stride = (long long)gridDim.x * 8;
   for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < n_items; it += stride) {
@@ -211,10 +215,12 @@ __global__ void __launch_bounds__(256) collect_kernel(const void *__restrict__ r
 }
 
 // one warp a pair: dy[t] (from L1 or L2 but for the token's first pair) against the pair's row
+template <int KD, int KR>
 __global__ void __launch_bounds__(256)
-collect_grad_kernel(const void *__restrict__ dy, int dy_type, const void *__restrict__ rows, int type, int T, int k,
-                    int H, const int32_t *__restrict__ row_of, const float *__restrict__ w,
-                    const int32_t *__restrict__ kept, void *__restrict__ d_rows, float *__restrict__ d_w) {
+collect_grad_kernel(const void *__restrict__ dy, int in_type, const void *rows, int rows_type, int T, int k, int H,
+                    const int32_t *__restrict__ row_of, const float *__restrict__ w, const int32_t *__restrict__ kept,
+                    void *d_rows, float *__restrict__ d_w) {
+  const int dy_type = known_type<KD>(in_type), type = known_type<KR>(rows_type);
   const int lane = threadIdx.x & 31, H8 = H >> 3, P = T * k;
   const long long stride = (long long)gridDim.x * 8, first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   for (long long p = first; p < P; p += stride) {
@@ -288,26 +294,48 @@ cudaError_t launch_sort_pairs(const int32_t *idx, int T, int k, int E, int32_t *
 cudaError_t launch_dispatch(const void *x, int type, int T, int k, int H, const int32_t *row_of, const int32_t *kept,
                             void *rows, cudaStream_t s) {
   KTimer kt_(KID_DISPATCH, s);
+  type = kernel_type(type, (const void *)((uintptr_t)x | (uintptr_t)rows));
   const int H8 = H / 8;
   dispatch_kernel<4><<<warp_grid((long long)T * ((H8 + 127) / 128)), 256, 0, s>>>(x, type, T, k, H, row_of, kept, rows);
   return cudaGetLastError();
 }
 
+// calls f with what is known of two types at compile time
+template <class F>
+cudaError_t by_types(int a, int b, const F &f) {
+  using std::integral_constant;
+  constexpr integral_constant<int, kAny> any{};
+  constexpr integral_constant<int, kF32Wide> w{};
+  constexpr integral_constant<int, k16> n{};
+  const int ka = known_of(a), kb = known_of(b);
+  if (ka == kAny || kb == kAny) return f(any, any);
+  if (ka == kF32Wide) return kb == kF32Wide ? f(w, w) : f(w, n);
+  return kb == kF32Wide ? f(n, w) : f(n, n);
+}
+
 cudaError_t launch_collect(const void *rows, int type, int T, int k, int H, const int32_t *row_of, const float *w,
                            const float *residual, void *y, int y_type, cudaStream_t s) {
   KTimer kt_(KID_COLLECT, s);
-  collect_kernel<<<warp_grid((long long)T * ((H / 8 + 31) / 32)), 256, 0, s>>>(rows, type, T, k, H, row_of, w, residual,
-                                                                             y, y_type);
-  return cudaGetLastError();
+  type = kernel_type(type, rows);
+  y_type = kernel_type(y_type, y);
+  return by_types(type, y_type, [&](auto r, auto o) {
+    collect_kernel<r.value, o.value><<<warp_grid((long long)T * ((H / 8 + 31) / 32)), 256, 0, s>>>(
+        rows, type, T, k, H, row_of, w, residual, y, y_type);
+    return cudaGetLastError();
+  });
 }
 
 cudaError_t launch_collect_grad(const void *dy, int dy_type, const void *rows, int type, int T, int k, int H,
                                 const int32_t *row_of, const float *w, const int32_t *kept, void *d_rows, float *d_w,
                                 cudaStream_t s) {
   KTimer kt_(KID_COLLECT_GRAD, s);
-  collect_grad_kernel<<<warp_grid((long long)T * k), 256, 0, s>>>(dy, dy_type, rows, type, T, k, H, row_of, w, kept,
-                                                                d_rows, d_w);
-  return cudaGetLastError();
+  type = kernel_type(type, (const void *)((uintptr_t)rows | (uintptr_t)d_rows));
+  dy_type = kernel_type(dy_type, dy);
+  return by_types(dy_type, type, [&](auto d, auto r) {
+    collect_grad_kernel<d.value, r.value><<<warp_grid((long long)T * k), 256, 0, s>>>(dy, dy_type, rows, type, T, k, H,
+                                                                                    row_of, w, kept, d_rows, d_w);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace moe
