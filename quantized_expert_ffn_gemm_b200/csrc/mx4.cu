@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const void *__restric
                                                           const int32_t *__restrict__ kept,
                                                           uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
   const int nb = K >> 5, P = T * k, type = known_type<KT>(x_type);
+  pdl_launch_dependents();
+  pdl_wait();
   const long long n = (long long)T * nb, stride = (long long)gridDim.x * 256;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
     Raw8 raw[4];
@@ -102,6 +104,8 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *__re
                                                             const uint8_t *__restrict__ scales, long long n,
                                                             void *__restrict__ out, int out_type) {
   const int type = known_type<KT>(out_type);
+  pdl_launch_dependents();
+  pdl_wait();
   const long long stride = (long long)gridDim.x * 256;
   constexpr int kAhead = 4;
   for (long long i0 = (long long)blockIdx.x * 256 + threadIdx.x; i0 < n; i0 += kAhead * stride) {
@@ -151,9 +155,8 @@ cudaError_t launch_mx4_quantize(const void *x, int type, int T, int K, const int
   KTimer kt_(KID_MX4_QUANTIZE, s);
   type = kernel_type(type, x);
   return by_type(type, [&](auto kt) {
-    mx4_quantize_kernel<kt.value><<<thread_grid((long long)T * (K / 32)), 256, 0, s>>>(
-        x, type, T, K, row_of, row_of ? k : 1, kept, codes, scales);
-    return cudaGetLastError();
+    return launch_pdl(mx4_quantize_kernel<kt.value>, dim3(thread_grid((long long)T * (K / 32))), dim3(256), 0, s, x, type,
+                      T, K, row_of, row_of ? k : 1, kept, codes, scales);
   });
 }
 
@@ -163,8 +166,8 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, l
   const long long n = rows * (K / 8);
   type = kernel_type(type, out);
   return by_type(type, [&](auto kt) {
-    mx4_dequantize_kernel<kt.value><<<thread_grid((n + 3) / 4), 256, 0, s>>>(codes, scales, n, out, type);
-    return cudaGetLastError();
+    return launch_pdl(mx4_dequantize_kernel<kt.value>, dim3(thread_grid((n + 3) / 4)), dim3(256), 0, s, codes, scales, n,
+                      out, type);
   });
 }
 

@@ -33,6 +33,8 @@ __global__ void __launch_bounds__(1024) pair_hist_kernel(const int32_t *__restri
                                                         int32_t *__restrict__ hist, Ctrl *ctrl) {
   extern __shared__ int32_t s_count[];
   for (int e = threadIdx.x; e < E; e += blockDim.x) s_count[e] = 0;
+  pdl_launch_dependents();
+  pdl_wait();
   __syncthreads();
   const long long p = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (p < P) {
@@ -54,6 +56,8 @@ pair_place_kernel(const int32_t *__restrict__ idx, int P, int k, int E, const in
   __shared__ int32_t s_kept;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5, chunks = gridDim.x;
   for (int i = tid; i < nw * E / 2; i += blockDim.x) reinterpret_cast<uint32_t *>(s_cnt)[i] = 0;  // nw is even
+  pdl_launch_dependents();
+  pdl_wait();
   __syncthreads();
   const long long p = (long long)blockIdx.x * blockDim.x + tid;
   const int e = p < P ? valid_expert(idx[p], E, ctrl) : -1;
@@ -78,6 +82,7 @@ pair_place_kernel(const int32_t *__restrict__ idx, int P, int k, int E, const in
     int before = 0, all = run;
     if (chunks > 1) {
       all = 0;
+#pragma unroll 16
       for (int c = 0; c < chunks; ++c) {
         const int n = hist[(size_t)c * E + x];
         before += c < (int)blockIdx.x ? n : 0;
@@ -151,6 +156,8 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const void *__restrict__ 
                                                       const int32_t *__restrict__ kept, void *__restrict__ rows) {
   const int lane = threadIdx.x & 31, H8 = H >> 3, nseg = (H8 + 32 * CH - 1) / (32 * CH), P = T * k;
   const int es = type_bytes(type);
+  pdl_launch_dependents();
+  pdl_wait();
   const long long n_items = (long long)T * nseg, stride = (long long)gridDim.x * 8;
   const long long first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   for (long long it = first; it < n_items; it += stride) {
@@ -174,43 +181,61 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const void *__restrict__ 
   zero_tail(rows, type, P, H8, kept, first, stride, lane);
 }
 
-// one warp a (token, segment of 32 chunks), four rows' loads in flight
-template <int KR, int KY>
+// One warp a (token, segment of 32 CH chunks), the segments of kLoads rows in flight. The rows are scattered over
+// memory, so a warp takes 2 KB of each (CH = 4) while that leaves work for every SM: 512 bytes at a time
+// read the rows of 8192 tokens at 4.7 TB/s, and eight rows in flight a lane at 3.
+template <int CH, int KR, int KY>
 __global__ void __launch_bounds__(256) collect_kernel(const void *__restrict__ rows, int rows_type, int T, int k, int H,
                                                      const int32_t *__restrict__ row_of, const float *__restrict__ w,
                                                      const float *residual, void *y, int out_type) {
   const int type = known_type<KR>(rows_type), y_type = known_type<KY>(out_type);
-  const int lane = threadIdx.x & 31, H8 = H >> 3, nseg = (H8 + 31) >> 5, P = T * k;
+  constexpr int kLoads = CH == 1 ? 4 : 2;
+  const int lane = threadIdx.x & 31, H8 = H >> 3, nseg = (H8 + 32 * CH - 1) / (32 * CH), P = T * k;
+  pdl_launch_dependents();
+  pdl_wait();
   const long long n_items = (long long)T * nseg, stride = (long long)gridDim.x * 8;
   for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < n_items; it += stride) {
-    const int t = (int)(it / nseg), c = (int)(it % nseg) * 32 + lane;
-    const bool cok = c < H8;
+    const int t = (int)(it / nseg), c0 = (int)(it % nseg) * 32 * CH + lane;
     int my_row = lane < k ? row_of[(size_t)t * k + lane] : -1;
     if (my_row >= P) my_row = -1;
     const float my_w = (w && lane < k) ? w[(size_t)t * k + lane] : 1.0f;
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (residual && cok) load8(residual, MOE_F32, ((size_t)t * H8 + c) * 8, acc);
-    for (int j0 = 0; j0 < k; j0 += 4) {
-      Raw8 v[4];
-      float wj[4];
-      int rj[4];
+    float acc[CH][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[c][q] = 0.0f;
+      if (residual && c0 + 32 * c < H8) load8(residual, MOE_F32, ((size_t)t * H8 + c0 + 32 * c) * 8, acc[c]);
+    }
+    for (int j0 = 0; j0 < k; j0 += kLoads) {
+      Raw8 v[kLoads][CH];
+      float wj[kLoads];
+      int rj[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
         rj[u] = __shfl_sync(0xffffffffu, my_row, (j0 + u) & 31);
         wj[u] = __shfl_sync(0xffffffffu, my_w, (j0 + u) & 31);
-        if (!cok || j0 + u >= k) rj[u] = -1;
-        if (rj[u] >= 0) v[u] = load_raw8(rows, type, ((size_t)rj[u] * H8 + c) * 8);
+        if (j0 + u >= k) rj[u] = -1;
+        if (rj[u] < 0) continue;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (c0 + 32 * c < H8) v[u][c] = load_raw8(rows, type, ((size_t)rj[u] * H8 + c0 + 32 * c) * 8);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kLoads; ++u) {
         if (rj[u] < 0) continue;  // a dropped pair adds nothing, whatever its weight is
-        float f[8];
-        raw8_to_float(v[u], type, f);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[q] = fmaf(wj[u], f[q], acc[q]);
+        for (int c = 0; c < CH; ++c) {
+          if (c0 + 32 * c >= H8) continue;
+          float f[8];
+          raw8_to_float(v[u][c], type, f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[c][q] = fmaf(wj[u], f[q], acc[c][q]);
+        }
       }
     }
-    if (cok) store8(y, y_type, ((size_t)t * H8 + c) * 8, acc);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (c0 + 32 * c < H8) store8(y, y_type, ((size_t)t * H8 + c0 + 32 * c) * 8, acc[c]);
   }
 }
 
@@ -221,6 +246,8 @@ collect_grad_kernel(const void *__restrict__ dy, int in_type, const void *rows, 
                     const int32_t *__restrict__ row_of, const float *__restrict__ w, const int32_t *__restrict__ kept,
                     void *d_rows, float *__restrict__ d_w) {
   const int dy_type = known_type<KD>(in_type), type = known_type<KR>(rows_type);
+  pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31, H8 = H >> 3, P = T * k;
   const long long stride = (long long)gridDim.x * 8, first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   for (long long p = first; p < P; p += stride) {
@@ -282,13 +309,14 @@ cudaError_t launch_sort_pairs(const int32_t *idx, int T, int k, int E, int32_t *
   if (e != cudaSuccess) return e;
   if (chunks > 1) {
     KTimer kt_(KID_PAIR_HIST, s);
-    pair_hist_kernel<<<chunks, threads, (size_t)E * 4, s>>>(idx, P, E, hist, ctrl);
+    const cudaError_t eh = launch_pdl(pair_hist_kernel, dim3(chunks), dim3(threads), (size_t)E * 4, s, idx, P, E, hist, ctrl);
+    if (eh != cudaSuccess) return eh;
   }
   {
     KTimer kt_(KID_PAIR_PLACE, s);
-    pair_place_kernel<<<chunks, threads, smem, s>>>(idx, P, k, E, hist, counts, offsets, row_of, src, ctrl);
+    return launch_pdl(pair_place_kernel, dim3(chunks), dim3(threads), smem, s, idx, P, k, E, (const int32_t *)hist, counts,
+                      offsets, row_of, src, ctrl);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_dispatch(const void *x, int type, int T, int k, int H, const int32_t *row_of, const int32_t *kept,
@@ -296,8 +324,8 @@ cudaError_t launch_dispatch(const void *x, int type, int T, int k, int H, const 
   KTimer kt_(KID_DISPATCH, s);
   type = kernel_type(type, (const void *)((uintptr_t)x | (uintptr_t)rows));
   const int H8 = H / 8;
-  dispatch_kernel<4><<<warp_grid((long long)T * ((H8 + 127) / 128)), 256, 0, s>>>(x, type, T, k, H, row_of, kept, rows);
-  return cudaGetLastError();
+  return launch_pdl(dispatch_kernel<4>, dim3(warp_grid((long long)T * ((H8 + 127) / 128))), dim3(256), 0, s, x, type, T, k,
+                    H, row_of, kept, rows);
 }
 
 // calls f with what is known of two types at compile time
@@ -318,10 +346,16 @@ cudaError_t launch_collect(const void *rows, int type, int T, int k, int H, cons
   KTimer kt_(KID_COLLECT, s);
   type = kernel_type(type, rows);
   y_type = kernel_type(y_type, y);
+  const int per = type == kF32Wide || type == MOE_F32 ? 2 : 4;  // chunks a lane for 2 KB of a row
+  const long long items = (long long)T * ((H / 8 + 32 * per - 1) / (32 * per));
+  const bool wide = items >= 16ll * num_sms();
   return by_types(type, y_type, [&](auto r, auto o) {
-    collect_kernel<r.value, o.value><<<warp_grid((long long)T * ((H / 8 + 31) / 32)), 256, 0, s>>>(
-        rows, type, T, k, H, row_of, w, residual, y, y_type);
-    return cudaGetLastError();
+    constexpr int CH = r.value == k16 ? 4 : 2;
+    if (wide)
+      return launch_pdl(collect_kernel<CH, r.value, o.value>, dim3(warp_grid(items)), dim3(256), 0, s, rows, type, T, k, H,
+                        row_of, w, residual, y, y_type);
+    return launch_pdl(collect_kernel<1, r.value, o.value>, dim3(warp_grid((long long)T * ((H / 8 + 31) / 32))), dim3(256),
+                      0, s, rows, type, T, k, H, row_of, w, residual, y, y_type);
   });
 }
 
@@ -332,9 +366,8 @@ cudaError_t launch_collect_grad(const void *dy, int dy_type, const void *rows, i
   type = kernel_type(type, (const void *)((uintptr_t)rows | (uintptr_t)d_rows));
   dy_type = kernel_type(dy_type, dy);
   return by_types(dy_type, type, [&](auto d, auto r) {
-    collect_grad_kernel<d.value, r.value><<<warp_grid((long long)T * k), 256, 0, s>>>(dy, dy_type, rows, type, T, k, H,
-                                                                                    row_of, w, kept, d_rows, d_w);
-    return cudaGetLastError();
+    return launch_pdl(collect_grad_kernel<d.value, r.value>, dim3(warp_grid((long long)T * k)), dim3(256), 0, s, dy,
+                      dy_type, rows, type, T, k, H, row_of, w, kept, d_rows, d_w);
   });
 }
 
