@@ -19,7 +19,7 @@
 //           commit: no loss while a stage's MMAs take 512, but 555 cycles a stage of an NC = 64
 //           tile, whose MMAs take 128. Three sets and 80 shared columns: the next tile began
 //           2000 cycles after a tile's end instead of 600.)
-//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warps 4-11 epilogue (two a lane quarter),
+//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warp 2 a fence, warps 4-11 epilogue (two a lane quarter),
 //           warps 12 on scales.
 //
 // Tiles are dealt round-robin with a group's row tiles innermost, so a weight tile is read from HBM once and
@@ -51,7 +51,7 @@ struct MxSmem {
   static constexpr int kOver = NC - kAcc1;  // columns that both accumulators use
   static_assert(kSf + kSfSets * kSfCols <= 512 && kOver % 16 == 0, "tensor memory");
   static constexpr int kBar = kStages * kStage;
-  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kNumBars = 3 * kStages + 5;
   static constexpr int kTiles = kBar + (kNumBars * 8 + 16 + 15) / 16 * 16;
   static constexpr int kPrefix = kTiles + kMxTileCache * 16;
   static constexpr int bytes(int E) { return kPrefix + (E + 1) * 4 + 1024; }
@@ -109,6 +109,9 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int type) {
   if (type == MOE_BF16) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -233,6 +236,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   auto acc_full = [&](int b) { return base + S::kBar + 8u * (2 * kStages + b); };
   auto acc_empty = [&](int b) { return base + S::kBar + 8u * (2 * kStages + 2 + b); };
   const uint32_t acc_over = base + S::kBar + 8u * (2 * kStages + 4);  // the shared columns are read
+  auto sf_in = [&](int s) { return base + S::kBar + 8u * (2 * kStages + 5 + s); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + S::kBar + S::kNumBars * 8);
   int32_t *s_pref = reinterpret_cast<int32_t *>(gbase + S::kPrefix);  // [E + 1] tiles before a group
   __shared__ int32_t s_warp[S::kThreads / 32];
@@ -241,7 +245,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   Ctrl *ctrl = args.ctrl;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 2);  // TMA's bytes, the stage's scale warp
+      mbar_init(full(s), 2);  // TMA's bytes, the scales through the fence warp
+      mbar_init(sf_in(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -256,14 +261,27 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (warp == 0 && elect_one()) {
+    prefetch_map(&tm_a);
+    prefetch_map(&tm_w);
+    if (UP) prefetch_map(&tm_u);
+  }
+  pdl_wait();
   {  // tiles before each group: every thread sums a run of groups, then a block scan of the runs
-    const int per = (args.E + S::kThreads - 1) / S::kThreads, g0 = tid * per, g1 = min(args.E, g0 + per);
-    int mine = 0;
-    for (int g = g0; g < g1; ++g) {
-      const int2 r = mx_group(args, g);
-      if (args.offsets && (r.x != args.offsets[g] || r.y != args.offsets[g + 1] || (g == 0 && r.x != 0)))
-        set_device_error(ctrl, MOE_ERR_DEVICE_CHECK, g);
-      mine += (r.y - r.x + kMxRows - 1) / kMxRows * args.n_tiles_n;
+    constexpr int kPer = (kMaxE + S::kThreads - 1) / S::kThreads;
+    const int per = (args.E + S::kThreads - 1) / S::kThreads, g0 = tid * per;
+    int at[kPer + 1], mine = 0;  // a run's offsets, loaded in one round
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i)
+      if (i <= per && g0 + i <= args.E) at[i] = args.offsets ? args.offsets[g0 + i] : i * args.n_rows;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int g = g0 + i;
+      if (i >= per || g >= args.E) continue;
+      const int s0 = min(max(at[i], 0), args.n_rows), s1 = min(max(at[i + 1], s0), args.n_rows);
+      if (s0 != at[i] || s1 != at[i + 1] || (g == 0 && s0 != 0)) set_device_error(ctrl, MOE_ERR_DEVICE_CHECK, g);
+      at[i] = (s1 - s0 + kMxRows - 1) / kMxRows * args.n_tiles_n;
+      mine += at[i];
     }
     int incl = mine;
 #pragma unroll
@@ -275,10 +293,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     __syncthreads();
     int run = incl - mine;
     for (int w = 0; w < warp; ++w) run += s_warp[w];
-    for (int g = g0; g < g1; ++g) {
-      const int2 r = mx_group(args, g);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int g = g0 + i;
+      if (i >= per || g >= args.E) continue;
       s_pref[g] = run;
-      run += (r.y - r.x + kMxRows - 1) / kMxRows * args.n_tiles_n;
+      run += at[i];
     }
     if (tid == S::kThreads - 1) s_pref[args.E] = run;
   }
@@ -373,10 +393,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
           ok = false;
           break;
         }
-        // The scale warps wrote through the generic proxy, tcgen05.cp reads through the async one: the fence
-        // between them stands here, on the path from their arrival to the copy. In the scale warps it
-        // waited for their loads in flight as well, which undid the fetching ahead.
-        fence_async_smem();
         tc_fence_after();
         const uint32_t sf = tmem + (uint32_t)(S::kSf + g % kBack * S::kSfCols);
         const uint64_t dsf = plain_desc(st_sf(s)), da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
@@ -403,6 +419,23 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     }
     // after a give-up: what was issued is complete before the columns are freed
     if (g > 0) (void)mbar_wait(empty((g - 1) % kStages), (uint32_t)((g - 1) / kStages) & 1u);
+  } else if (warp == 2) {
+    // ------------------------------------------------ proxy fence
+    // The scale warps write through the generic proxy, tcgen05.cp reads through the async one. The fence between
+    // them stands on the path from one to the other, in a warp of its own: in the scale warps it waited for
+    // their loads in flight as well, in the MMA warp it was a good part of a stage's issue.
+    const int total_g = n_my * nk;
+    for (int g = 0; g < total_g; ++g) {
+      const int s = g % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(sf_in(s), (uint32_t)(g / kStages) & 1u))) {
+        if (lane == 0) mx_timeout(ctrl, 46);
+        break;
+      }
+      if (lane == 0) {
+        fence_async_smem();
+        mbar_arrive(full(s));
+      }
+    }
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------ epilogue: a lane quarter and every other 16 features
     const int q = warp & 3, half = (warp - 4) >> 2;
@@ -502,7 +535,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(s));
+      if (lane == 0) mbar_arrive(sf_in(s));
       return true;
     };
     scales.run(warp - 12, put);
@@ -535,6 +568,11 @@ cudaError_t launch_nc(const Mx4ProductArgs &p, cudaStream_t s) {
   const cudaError_t e = smem_limit_once(mx4_product_kernel<NC, UP>, MxSmem<NC>::bytes(kMaxE));
   if (e != cudaSuccess) return e;
   KTimer kt_(KID_MX4_PRODUCT, s);
+  // A short product begins while its predecessor ends (four tokens: 0.5 us). A long one gains nothing, and with
+  // its blocks waiting beside the quantiser's the two took 173-180 us for 8192 tokens, not 172.
+  if (p.n_rows <= 4096)
+    return launch_pdl(mx4_product_kernel<NC, UP>, dim3(grid), dim3(MxSmem<NC>::kThreads), MxSmem<NC>::bytes(p.E), s, ta,
+                      tw, tu, a);
   mx4_product_kernel<NC, UP><<<grid, MxSmem<NC>::kThreads, MxSmem<NC>::bytes(p.E), s>>>(ta, tw, tu, a);
   return cudaGetLastError();
 }
