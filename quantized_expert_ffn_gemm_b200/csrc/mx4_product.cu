@@ -580,16 +580,20 @@ cudaError_t launch_nc(const Mx4ProductArgs &p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mx4_product(const Mx4ProductArgs &p, cudaStream_t s) {
-  // columns of a tile: as many as leave four tiles an SM, so that the last round's idle SMs cost little
+  // Columns of a tile. 256: fewest bytes from L2 and the MMAs' best rate, for groups of many rows (8192 tokens
+  // over 512 experts, 160 rows each: 171 us with the quantiser, 189 with 128). 128: less left over at the
+  // end and an epilogue of two accumulators, for the others (2048 tokens, down, 40 rows each: 68.5 us, 70.5 with
+  // 256; four tokens: 21.0 us cold, 22.6). 64: more SMs at work where 128 leaves some idle (four groups of
+  // 64 rows, K = 4096, N = 1024: 14.4 us, 16.0 with 128, 18.5 with 256).
   const bool up = p.up_codes != nullptr;
   const int live = p.E < p.n_rows ? p.E : p.n_rows;
-  auto tiles = [&](int nc) {
+  auto tiles = [&](int nc) {  // at most: every live group's last tile is partial
     const int feat = up ? nc / 2 : nc;
     return ((long long)p.n_rows / kMxRows + live) * ((p.N + feat - 1) / feat);
   };
-  const long long want = 4ll * num_sms();
-  if (tiles(256) >= want) return up ? launch_nc<256, true>(p, s) : launch_nc<256, false>(p, s);
-  if (tiles(128) >= want) return up ? launch_nc<128, true>(p, s) : launch_nc<128, false>(p, s);
+  if (tiles(256) >= 4ll * num_sms() && p.n_rows >= 64ll * p.E)
+    return up ? launch_nc<256, true>(p, s) : launch_nc<256, false>(p, s);
+  if (tiles(128) >= num_sms()) return up ? launch_nc<128, true>(p, s) : launch_nc<128, false>(p, s);
   return up ? launch_nc<64, true>(p, s) : launch_nc<64, false>(p, s);
 }
 
