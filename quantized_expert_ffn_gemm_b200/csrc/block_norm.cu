@@ -22,6 +22,7 @@ namespace moe {
 
 namespace {
 
+constexpr int kGradBlocks = 2;  // blocks of 256 threads an SM holds in the gradient (three leave two rows each: 80 us)
 constexpr int kNormWarps = 16;  // a block has 256 threads, or 512 for rows of more than 2048 values
 
 // Sum over the tpr threads of a row (a power of two from 32 to 512); every thread of the block calls it.
@@ -160,19 +161,242 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 3 : 1) block_norm_kernel(const
   }
 }
 
-// With one chunk a thread the row stays in registers, the next one loaded behind it; with more, each of the three
-// passes reads it again (from L2) and works g out again.
-template <int KT, int CH, int R, int Y, int U>
-__global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(const BlockNormGradArgs a, float *__restrict__ part, int tpr) {
-  constexpr bool kOne = CH == 1;
+// Four values of a row, fp32 or 16-bit, as the gradient's rows pass through shared memory.
+template <bool F>
+__device__ __forceinline__ void get4(const uint8_t *plane, int i, bool bf16, float v[4]) {
+  if constexpr (F) {
+    const float4 x = reinterpret_cast<const float4 *>(plane)[i];
+    v[0] = x.x;
+    v[1] = x.y;
+    v[2] = x.z;
+    v[3] = x.w;
+  } else {
+    const uint2 w = reinterpret_cast<const uint2 *>(plane)[i];
+    const uint32_t p[2] = {w.x, w.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (bf16) {
+        v[2 * j] = __uint_as_float(p[j] << 16);
+        v[2 * j + 1] = __uint_as_float(p[j] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[j]));
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    }
+  }
+}
+template <bool F>
+__device__ __forceinline__ void put4(void *base, size_t i, bool bf16, const float v[4]) {
+  if constexpr (F) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(base) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t p[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (bf16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        p[j] = *reinterpret_cast<const uint32_t *>(&b);
+      } else {
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        p[j] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) = make_uint2(p[0], p[1]);
+  }
+}
+// this thread's four values of a row to their place in a plane (16 or 8 bytes, without passing registers)
+template <bool F>
+__device__ __forceinline__ void copy4(uint8_t *plane, int i, const void *base, size_t at) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(plane) + (uint32_t)i * (F ? 16u : 8u);
+  if constexpr (F)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(static_cast<const float *>(base) + at) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(static_cast<const uint16_t *>(base) + at) : "memory");
+}
+__device__ __forceinline__ void ring_wait(int newer) {  // all but the `newer` youngest groups have landed
+  if (newer >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (newer == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (newer == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+constexpr int kRingStages = 4;
+
+// Rows of up to 8 tpr values, two groups of four a thread (values 4 lane .. and 4 tpr + 4 lane ..: accesses are whole
+// lines for every type). RF, YF, UF: r (and its gradients), y, u are fp32, else 16-bit. A row takes two
+// dependent sums, so the rows to come pass through a ring in shared memory meanwhile: each thread copies and
+// reads its own values, no barrier needed. (The next row held in registers left room for 16 warps an SM
+// and took 69 us for 8192 rows of 2048.)
+template <int KT, bool RF, bool YF, bool UF>
+__global__ void __launch_bounds__(KT, KT == 256 ? kGradBlocks : 1)
+block_norm_grad_kernel(const BlockNormGradArgs a, float *__restrict__ part, int tpr, int stages) {
+  extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_sum[2][kNormWarps];
   RowSum row_sum{s_sum, tpr, 0};
-  const int rows = KT / tpr, sub = threadIdx.x / tpr, lane = threadIdx.x & (tpr - 1), H8 = a.H >> 3;
-  const int rt = known_type<R>(a.r_type), dt = known_type<R>(a.d_type), drt = known_type<R>(a.dr_type),
-            yt = known_type<Y>(a.y_type), dyt = known_type<Y>(a.dy_type), ut = known_type<U>(a.u_type),
-            gt = R == kAny ? a.gain_type : kF32Wide;
+  constexpr int kR = KT * (RF ? 32 : 16), kU = KT * (UF ? 32 : 16), kY = KT * (YF ? 32 : 16);
+  constexpr int kD0 = kR, kU0 = 2 * kR, kY0 = 2 * kR + kU, kBytes = 2 * kR + kU + kY;
+  const int rows = KT / tpr, sub = threadIdx.x / tpr, lane = threadIdx.x & (tpr - 1);
+  const bool rb = a.r_type == MOE_BF16, yb = a.y_type == MOE_BF16, ub = a.u_type == MOE_BF16;
   const float inv_h = 1.0f / (float)a.H;
   const int stride = gridDim.x * rows, first = blockIdx.x * rows + sub;
+  const int at[2] = {4 * lane, 4 * tpr + 4 * lane};
+  const bool in[2] = {at[0] < a.H, at[1] < a.H};
+  float sum_v[2][4], sum_x[2][4];  // sum over this thread's rows of g v (a token's gate folded in) and du x
+  float pre[2][4], f[2][4];        // pre_gain; post_gain times a channel's gate
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      sum_v[g][q] = sum_x[g][q] = 0.0f;
+      pre[g][q] = f[g][q] = 1.0f;
+    }
+  pdl_launch_dependents();
+  pdl_wait();
+  auto fetch = [&](long long t, int s) {
+    if (t < a.T) {
+      uint8_t *m = s_ring + s * kBytes;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (!in[g]) continue;
+        const size_t i = (size_t)t * a.H + at[g];
+        const int slot = g * KT + threadIdx.x;
+        if (a.du) {
+          copy4<RF>(m, slot, a.r, i);
+          copy4<UF>(m + kU0, slot, a.du, i);
+        }
+        if (a.dr_out) copy4<RF>(m + kD0, slot, a.dr_out, i);
+        if (a.y) copy4<YF>(m + kY0, slot, a.y, i);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int s = 0; s + 1 < stages; ++s) fetch(first + (long long)s * stride, s);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if (!in[g]) continue;
+    float w[4];
+    if (a.pre_gain) get4<true>(reinterpret_cast<const uint8_t *>(a.pre_gain), at[g] / 4, false, pre[g]);
+    if (a.post_gain) get4<true>(reinterpret_cast<const uint8_t *>(a.post_gain), at[g] / 4, false, f[g]);
+    if (a.gate_mode == MOE_GATE_CHANNEL) {
+      get4<true>(reinterpret_cast<const uint8_t *>(a.gate), at[g] / 4, false, w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[g][q] *= w[q];
+    }
+  }
+  float su_n = 0.0f, sy_n = 1.0f, tok_n = 1.0f;  // the next row's statistics and gate
+  auto stats = [&](long long t) {
+    if (t >= a.T) return;
+    if (a.du) su_n = a.rstd_u[t];
+    if (a.y && a.post_norm) sy_n = a.rstd_y[t];
+    if (a.gate_mode == MOE_GATE_TOKEN) tok_n = a.gate[t];
+  };
+  stats(first);
+  int stage = 0;
+  for (long long t = first; t - sub < a.T; t += stride) {  // every thread of the block stays for the sums
+    const bool live = t < a.T;
+    const size_t base = (size_t)t * a.H;
+    const float su = su_n, sy = sy_n, tok = tok_n;
+    stats(t + stride);
+    fetch(t + (long long)(stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
+    ring_wait(stages - 1);
+    const uint8_t *m = s_ring + stage * kBytes;
+    float x[2][4], h[2][4], m_u = 0.0f;
+    if (a.du) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (!(live && in[g])) continue;
+        const int slot = g * KT + threadIdx.x;
+        get4<RF>(m, slot, rb, x[g]);
+        get4<UF>(m + kU0, slot, ub, h[g]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x[g][q] *= su;
+          const float ux = h[g][q] * x[g][q];
+          sum_x[g][q] += ux;
+          m_u = fmaf(pre[g][q], ux, m_u);
+          h[g][q] *= pre[g][q];
+        }
+      }
+      m_u = row_sum(m_u) * inv_h;
+    }
+    float m_y = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {  // h becomes g, then gate post_gain g; x becomes v
+      if (!(live && in[g])) continue;
+      const int slot = g * KT + threadIdx.x;
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.dr_out) get4<RF>(m + kD0, slot, rb, d);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        h[g][q] = a.du ? fmaf(su, fmaf(-x[g][q], m_u, h[g][q]), d[q]) : d[q];
+        d[q] = a.res_scale * h[g][q];
+      }
+      put4<RF>(a.dr, base + at[g], rb, d);
+      if (a.y) {
+        get4<YF>(m + kY0, slot, yb, x[g]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x[g][q] *= sy;
+          const float hv = h[g][q] * x[g][q];
+          sum_v[g][q] = fmaf(tok, hv, sum_v[g][q]);
+          m_y = fmaf(f[g][q], hv, m_y);
+          h[g][q] *= f[g][q];
+        }
+      }
+    }
+    if (a.y) {
+      const bool token_grad = a.d_gate && a.gate_mode == MOE_GATE_TOKEN;
+      if (a.post_norm || token_grad) m_y = row_sum(m_y);
+      if (token_grad && live && lane == 0) a.d_gate[t] = m_y;
+      const float mean = a.post_norm ? m_y * inv_h : 0.0f, scale = sy * tok;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (!(live && in[g])) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[g][q] = scale * fmaf(-x[g][q], mean, h[g][q]);
+        put4<YF>(a.dy, base + at[g], yb, h[g]);
+      }
+    }
+    stage = stage + 1 == stages ? 0 : stage + 1;
+  }
+  if (!part) return;
+  // this block's sums: the row groups joined in shared memory in order, then one row of partials
+  if (rows > 1) {
+    __shared__ float s_p[2][128 * 8];
+    for (int r = 0; r < rows; ++r) {
+      __syncthreads();
+      if (sub != r) continue;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float *pv = &s_p[0][at[g] + q], *px = &s_p[1][at[g] + q];
+          *pv = sum_v[g][q] += r ? *pv : 0.0f;
+          *px = sum_x[g][q] += r ? *px : 0.0f;
+        }
+    }
+    if (sub != rows - 1) return;
+  }
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if (!in[g]) continue;
+    float *p = part + (size_t)blockIdx.x * 2 * a.H + at[g];
+    put4<true>(p, 0, false, sum_v[g]);
+    put4<true>(p, a.H, false, sum_x[g]);
+  }
+}
+
+// Rows of more than 4096 values: CH chunks of eight a thread; each of the three passes reads the row again (from L2)
+// and works g out again.
+template <int CH>
+__global__ void __launch_bounds__(512, 1) block_norm_grad_long_kernel(const BlockNormGradArgs a, float *__restrict__ part) {
+  constexpr int tpr = 512;
+  __shared__ float s_sum[2][kNormWarps];
+  RowSum row_sum{s_sum, tpr, 0};
+  const int lane = threadIdx.x, H8 = a.H >> 3;
+  const int rt = a.r_type, dt = a.d_type, drt = a.dr_type, yt = a.y_type, dyt = a.dy_type, ut = a.u_type,
+            gt = a.gain_type;
+  const float inv_h = 1.0f / (float)a.H;
   float sum_v[CH][8], sum_x[CH][8];  // sum over this thread's rows of g v (a token's gate folded in) and du x
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -198,17 +422,10 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(
     if (a.dr_out) w.d = load_raw8(a.dr_out, dt, at);
     if (a.y) w.y = load_raw8(a.y, yt, at);
   };
-  Row w, next;
-  if constexpr (kOne) fetch(first, lane, next);
-  for (long long t = first; t - sub < a.T; t += stride) {  // every thread of the block stays for the sums
-    const bool live = t < a.T;
+  Row w;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t base = (size_t)t * a.H;
-    if constexpr (kOne) {
-      w = next;
-      fetch(t + stride, lane, next);
-    } else {
-      fetch(t, H8, w);
-    }
+    fetch(t, H8, w);
     const float rstd_u = w.su, rstd_y = w.sy, tok = w.tok;
     // x = r' rstd_u and h = du pre_gain (u: du)
     float x[8], h[8], m_u = 0.0f;
@@ -226,8 +443,8 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = lane + c * tpr;
-        if (!(live && i < H8)) continue;
-        if constexpr (!kOne) fetch(t, i, w);
+        if (i >= H8) continue;
+        fetch(t, i, w);
         float u[8];
         xh(i, u);
 #pragma unroll
@@ -241,18 +458,16 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(
     // g: the stream's gradient (into h), res_scale g to dr
     auto grad = [&](int i) {
       float d[8];
-      if constexpr (!kOne) {
-        float u[8];
-        if (a.du) xh(i, u);
+      float u[8];
+      if (a.du) xh(i, u);
+      if (!a.dr_out) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[q] = 0.0f;
+      } else {
+        raw8_to_float(w.d, dt, d);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        d[q] = 0.0f;
-        h[q] = a.du ? rstd_u * fmaf(-x[q], m_u, h[q]) : 0.0f;
-      }
-      if (a.dr_out) raw8_to_float(w.d, dt, d);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) h[q] += d[q];
+      for (int q = 0; q < 8; ++q) h[q] = a.du ? fmaf(rstd_u, fmaf(-x[q], m_u, h[q]), d[q]) : d[q];
     };
     auto put_dr = [&](int i) {
       float d[8];
@@ -265,84 +480,51 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 2 : 1) block_norm_grad_kernel(
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = lane + c * tpr;
-      if (!(live && i < H8)) continue;
-      if constexpr (!kOne) fetch(t, i, w);
+      if (i >= H8) continue;
+      fetch(t, i, w);
       grad(i);
-      if (kOne || !a.y) put_dr(i);
+      if (!a.y) put_dr(i);
       if (a.y) {
         raw8_to_float(w.y, yt, v);
         load_post(a, gt, i, f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           v[q] *= rstd_y;
-          sum_v[c][q] = fmaf(tok * h[q], v[q], sum_v[c][q]);
+          const float hv = h[q] * v[q];
+          sum_v[c][q] = fmaf(tok, hv, sum_v[c][q]);
+          m_y = fmaf(f[q], hv, m_y);
           f[q] *= h[q];
-          m_y = fmaf(f[q], v[q], m_y);
         }
       }
     }
     if (a.y) {
       const bool token_grad = a.d_gate && a.gate_mode == MOE_GATE_TOKEN;
       if (a.post_norm || token_grad) m_y = row_sum(m_y);
-      if (token_grad && live && lane == 0) a.d_gate[t] = m_y;
-      const float mean = a.post_norm ? m_y * tok * inv_h : 0.0f;
+      if (token_grad && lane == 0) a.d_gate[t] = m_y;
+      const float mean = a.post_norm ? m_y * inv_h : 0.0f, scale = rstd_y * tok;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = lane + c * tpr;
-        if (!(live && i < H8)) continue;
-        if constexpr (!kOne) {
-          fetch(t, i, w);
-          grad(i);
-          put_dr(i);
-          raw8_to_float(w.y, yt, v);
-          load_post(a, gt, i, f);
+        if (i >= H8) continue;
+        fetch(t, i, w);
+        grad(i);
+        put_dr(i);
+        raw8_to_float(w.y, yt, v);
+        load_post(a, gt, i, f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            v[q] *= rstd_y;
-            f[q] *= h[q];
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] = rstd_y * fmaf(-v[q], mean, tok * f[q]);
+        for (int q = 0; q < 8; ++q) f[q] = scale * fmaf(-(v[q] * rstd_y), mean, f[q] * h[q]);
         store8(a.dy, dyt, base + 8 * i, f);
       }
     }
   }
   if (!part) return;
-  // this block's sums: the row groups joined in shared memory in order, then one row of partials
-  if (rows == 1) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = lane + c * tpr;
-      if (i >= H8) continue;
-      float *p = part + (size_t)blockIdx.x * 2 * a.H + 8 * i;
-      store8(p, kF32Wide, 0, sum_v[c]);
-      store8(p + a.H, kF32Wide, 0, sum_x[c]);
-    }
-  } else if constexpr (kOne) {  // short rows are one chunk a thread
-    __shared__ float s_p[2][128 * 8];
-    for (int g = 0; g < rows; ++g) {
-      __syncthreads();
-      if (sub == g && lane < H8) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float *pv = &s_p[0][q * tpr + lane], *px = &s_p[1][q * tpr + lane];
-          *pv = (g ? *pv : 0.0f) + sum_v[0][q];
-          *px = (g ? *px : 0.0f) + sum_x[0][q];
-        }
-      }
-    }
-    if (sub == rows - 1 && lane < H8) {
-      float sv[8], sx[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        sv[q] = s_p[0][q * tpr + lane];
-        sx[q] = s_p[1][q * tpr + lane];
-      }
-      float *p = part + (size_t)blockIdx.x * 2 * a.H + 8 * lane;
-      store8(p, kF32Wide, 0, sv);
-      store8(p + a.H, kF32Wide, 0, sx);
-    }
+  for (int c = 0; c < CH; ++c) {
+    const int i = lane + c * tpr;
+    if (i >= H8) continue;
+    float *p = part + (size_t)blockIdx.x * 2 * a.H + 8 * i;
+    store8(p, kF32Wide, 0, sum_v[c]);
+    store8(p + a.H, kF32Wide, 0, sum_x[c]);
   }
 }
 
@@ -396,7 +578,7 @@ int blocks_of(int T, int H, int per_sm) {  // per_sm: blocks of 256 threads an S
   return want < cap ? want : cap;
 }
 int norm_blocks(int T, int H) { return blocks_of(T, H, threads_of(H) == 256 ? 3 : 2); }
-int grad_blocks(int T, int H) { return blocks_of(T, H, 2); }
+int grad_blocks(int T, int H) { return blocks_of(T, H, threads_of(H) == 256 ? kGradBlocks : 2); }
 
 // calls f with the kernel's template arguments: types are told apart at compile time for rows of one chunk a
 // thread whose fp32 tensors are 32-byte aligned
@@ -420,6 +602,33 @@ cudaError_t by_types(int H, int r, int y, int u, bool wide_gains, const F &f) {
     return u == kF32Wide ? f(kt, one, n, n, w) : f(kt, one, n, n, n);
   };
   return threads_of(H) == 256 ? typed(integral_constant<int, 256>{}) : typed(t512);
+}
+
+template <int KT, bool RF, bool YF, bool UF>
+cudaError_t run_grad(const BlockNormGradArgs &a, float *part, int grid, cudaStream_t s) {
+  constexpr int kBytes = KT * (2 * (RF ? 32 : 16) + (YF ? 32 : 16) + (UF ? 32 : 16));
+  constexpr int kFit = 208 * 1024 / (KT == 256 ? kGradBlocks : 1) / kBytes;
+  const int tpr = tpr_of(a.H), rows = (a.T + KT / tpr - 1) / (KT / tpr);
+  int stages = kFit < kRingStages ? kFit : kRingStages;
+  if (stages > (rows + grid - 1) / grid) stages = (rows + grid - 1) / grid;  // no more than a block's rows
+  static_assert(kFit >= 1, "a row fits");
+  const cudaError_t e = smem_limit_once(block_norm_grad_kernel<KT, RF, YF, UF>, kRingStages * kBytes < 208 * 1024
+                                                                                   ? kRingStages * kBytes
+                                                                                   : 208 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(block_norm_grad_kernel<KT, RF, YF, UF>, dim3(grid), dim3(KT), (size_t)stages * kBytes, s, a, part, tpr,
+                    stages);
+}
+
+template <int KT>
+cudaError_t grad_by_types(const BlockNormGradArgs &a, float *part, int grid, cudaStream_t s) {
+  const bool r = a.r_type == MOE_F32, y = a.y && a.y_type == MOE_F32, u = a.du && a.u_type == MOE_F32;
+  if (r) {
+    if (y) return u ? run_grad<KT, true, true, true>(a, part, grid, s) : run_grad<KT, true, true, false>(a, part, grid, s);
+    return u ? run_grad<KT, true, false, true>(a, part, grid, s) : run_grad<KT, true, false, false>(a, part, grid, s);
+  }
+  if (y) return u ? run_grad<KT, false, true, true>(a, part, grid, s) : run_grad<KT, false, true, false>(a, part, grid, s);
+  return u ? run_grad<KT, false, false, true>(a, part, grid, s) : run_grad<KT, false, false, false>(a, part, grid, s);
 }
 
 // what is known of a type: of the tensors that share it all have to be 32-byte aligned; one that is absent
@@ -467,11 +676,10 @@ cudaError_t launch_block_norm_grad(const BlockNormGradArgs &args, float *scratch
   cudaError_t e;
   {
     KTimer kt_(KID_BLOCK_NORM_GRAD, s);
-    e = by_types(a.H, known(args.r_type, {a.r, a.dr_out, a.dr}), known(args.y_type, {a.y, a.dy}),
-                 known(args.u_type, {a.du}), a.gain_type == kF32Wide, [&](auto kt, auto ch, auto r, auto y, auto u) {
-                   return launch_pdl(block_norm_grad_kernel<kt.value, ch.value, r.value, y.value, u.value>, dim3(grid),
-                                     dim3(threads_of(a.H)), 0, s, a, part, tpr_of(a.H));
-                 });
+    if (a.H > 8192) e = launch_pdl(block_norm_grad_long_kernel<4>, dim3(grid), dim3(512), 0, s, a, part);
+    else if (a.H > 4096) e = launch_pdl(block_norm_grad_long_kernel<2>, dim3(grid), dim3(512), 0, s, a, part);
+    else if (threads_of(a.H) == 256) e = grad_by_types<256>(args, part, grid, s);
+    else e = grad_by_types<512>(args, part, grid, s);
   }
   if (e == cudaSuccess && sums) {
     KTimer kt_(KID_BLOCK_NORM_GAIN, s);
