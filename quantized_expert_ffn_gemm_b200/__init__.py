@@ -6,7 +6,8 @@ be loaded, importing works but every call raises (there is no fallback path).
 
 Entry points mirror include/moe_ffn.h: rmsnorm_bf16, router_topk, permute, expert_ffn, combine,
 layer_forward, stack_forward, dequant_rows, read_device_error, plus a Workspace helper; the block
-operators (norms around a block, sorted pairs, their gradients, MXFP4) are in block.py.
+operators (norms around a block, sorted pairs, their gradients, MXFP4) are in block.py, over the
+compiled binding _bind.so.
 """
 from __future__ import annotations
 
@@ -74,7 +75,7 @@ def lib():
         _lib.moe_workspace_bytes.argtypes = [ctypes.POINTER(LayerDesc), ctypes.c_int32]
         for name in EXPORTED[2:]:
             getattr(_lib, name).restype = ctypes.c_int32
-        _block.bind(_lib, _raw_stream, MoeError)
+        _block.bind(_lib)
         _lib.moe_kernel_name.restype = ctypes.c_char_p
         _lib.moe_kernel_name.argtypes = [ctypes.c_int32]
     return _lib
