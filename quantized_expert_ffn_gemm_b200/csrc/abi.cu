@@ -36,7 +36,7 @@ const char *const kKernelNames[KID_COUNT] = {
     "router_decode", "router_gemm", "topk", "perm_hist", "perm_scan", "perm_scatter", "perm_gather", "combine", "rmsnorm", "dequant_rows", "dec_units", "dec_gate_up", "dec_down",
     "tile_list", "gemm_gate_up", "gemm_down", "router_split", "router_tc", "decode_fused", "mmq_quant",
     "mmq_gate_up", "mid_plan", "mid_expert", "mid_combine", "block_norm", "block_norm_grad",
-    "block_norm_gain", "pair_hist", "pair_place", "dispatch", "collect", "collect_grad", "mx4_quantize",
+    "block_norm_gain", "pair_hist", "pair_scan", "pair_place", "dispatch", "collect", "collect_grad", "mx4_quantize",
     "mx4_dequantize", "mx4_product"};
 }  // namespace
 

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *__re
                                                             const uint8_t *__restrict__ scales, long long n,
                                                             void *__restrict__ out, int out_type) {
   const int type = known_type<KT>(out_type);
-  pdl_launch_dependents();
+  // its dependents start when it ends: what it writes may be router weights, which a layer call reads early
   pdl_wait();
   const long long stride = (long long)gridDim.x * 256;
   constexpr int kAhead = 4;

@@ -45,9 +45,36 @@ __global__ void __launch_bounds__(1024) pair_hist_kernel(const int32_t *__restri
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(size_t)blockIdx.x * E + e] = s_count[e];
 }
 
-// one chunk a block; with one chunk in all, hist is not read
+// Many chunks: each expert's counts become the pairs in the chunks before, hist[chunks][e] their total. 32
+// experts a block, a warp of lanes apiece over runs of chunks.
+__global__ void __launch_bounds__(1024) pair_scan_kernel(int32_t *__restrict__ hist, int chunks, int E) {
+  __shared__ int32_t s_run[32][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int per = (chunks + 31) / 32, c0 = run * per, c1 = min(chunks, c0 + per);
+  pdl_launch_dependents();
+  pdl_wait();
+  int sum = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) sum += hist[(size_t)c * E + e];
+  }
+  s_run[run][lane] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int r = 0; r < run; ++r) before += s_run[r][lane];
+  if (e >= E) return;
+  for (int c = c0; c < c1; ++c) {
+    const int n = hist[(size_t)c * E + e];
+    hist[(size_t)c * E + e] = before;
+    before += n;
+  }
+  if (run == 31) hist[(size_t)chunks * E + e] = before;
+}
+
+// One chunk a block; with one chunk in all hist is not read, with few (scanned = 0) every block adds up the
+// chunks' counts itself, which spares a launch, with many it finds them added up.
 __global__ void __launch_bounds__(1024)
-pair_place_kernel(const int32_t *__restrict__ idx, int P, int k, int E, const int32_t *__restrict__ hist,
+pair_place_kernel(const int32_t *__restrict__ idx, int P, int k, int E, const int32_t *__restrict__ hist, int scanned,
                   int32_t *__restrict__ counts, int32_t *__restrict__ offsets, int32_t *__restrict__ row_of,
                   int32_t *__restrict__ src, Ctrl *ctrl) {
   extern __shared__ int32_t s_base[];                         // [E] first row of this chunk's pairs of e
@@ -80,7 +107,10 @@ pair_place_kernel(const int32_t *__restrict__ idx, int P, int k, int E, const in
       run += n;
     }
     int before = 0, all = run;
-    if (chunks > 1) {
+    if (scanned) {
+      before = hist[(size_t)blockIdx.x * E + x];
+      all = hist[(size_t)chunks * E + x];
+    } else if (chunks > 1) {
       all = 0;
 #pragma unroll 16
       for (int c = 0; c < chunks; ++c) {
@@ -296,14 +326,17 @@ int warp_grid(long long items) {  // eight warps a block
 
 }  // namespace
 
+constexpr int kScanChunks = 128;  // chunks from which the scan kernel is worth its launch
+
 size_t sort_pairs_scratch(long long P, int E) {
   const int per = 32 * chunk_warps(E);
-  return (size_t)((P + per - 1) / per) * E * 4;
+  return (size_t)((P + per - 1) / per + 1) * E * 4;
 }
 
 cudaError_t launch_sort_pairs(const int32_t *idx, int T, int k, int E, int32_t *counts, int32_t *offsets,
                               int32_t *row_of, int32_t *src, int32_t *hist, Ctrl *ctrl, cudaStream_t s) {
-  const int P = T * k, nw = chunk_warps(E), threads = 32 * nw, chunks = (P + threads - 1) / threads;
+  const int P = T * k, nw = chunk_warps(E), threads = 32 * nw, chunks = (int)(((long long)P + threads - 1) / threads);
+  const int scanned = chunks > kScanChunks ? 1 : 0;
   const size_t smem = (size_t)E * 4 + (size_t)nw * E * 2;
   const cudaError_t e = smem_limit_once(pair_place_kernel, smem > 48 * 1024 ? 160 * 1024 : 0);
   if (e != cudaSuccess) return e;
@@ -312,9 +345,14 @@ cudaError_t launch_sort_pairs(const int32_t *idx, int T, int k, int E, int32_t *
     const cudaError_t eh = launch_pdl(pair_hist_kernel, dim3(chunks), dim3(threads), (size_t)E * 4, s, idx, P, E, hist, ctrl);
     if (eh != cudaSuccess) return eh;
   }
+  if (scanned) {
+    KTimer kt_(KID_PAIR_SCAN, s);
+    const cudaError_t es = launch_pdl(pair_scan_kernel, dim3((E + 31) / 32), dim3(1024), 0, s, hist, chunks, E);
+    if (es != cudaSuccess) return es;
+  }
   {
     KTimer kt_(KID_PAIR_PLACE, s);
-    return launch_pdl(pair_place_kernel, dim3(chunks), dim3(threads), smem, s, idx, P, k, E, (const int32_t *)hist, counts,
+    return launch_pdl(pair_place_kernel, dim3(chunks), dim3(threads), smem, s, idx, P, k, E, (const int32_t *)hist, scanned, counts,
                       offsets, row_of, src, ctrl);
   }
 }

@@ -182,3 +182,14 @@ def test_product_on_a_stream_and_in_a_graph():
 def test_product_many_tiles(groups, K, N, up):
     """Several tiles a block, of every tile width, full and partial rows and columns."""
     check_product([(37 * i) % 200 for i in range(groups)], K, N, up, BF16)
+
+
+def test_product_flags_offsets_that_are_no_offsets():
+    """Offsets that run back or past the rows are clamped to them and flagged; nothing outside is touched."""
+    a, w, _, offsets = rows_and_weights([30, 20, 14], 256, 64, False)
+    ws = moe.Workspace(256)
+    good = moe.mx4_product(a, w, offsets.cuda(), ws=ws)
+    for bad in ([0, 30, 20, 64], [0, 30, 50, 100], [-5, 30, 50, 64], [3, 30, 50, 64]):
+        moe.mx4_product(a, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), ws=ws)
+        assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_CHECK, bad
+    assert torch.equal(good, moe.mx4_product(a, w, offsets.cuda(), ws=ws)) and moe.read_device_error(ws) == 0

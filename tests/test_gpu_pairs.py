@@ -44,6 +44,27 @@ def test_sort(T, k, E, drop):
     assert moe.read_device_error(ws) == 0
 
 
+@pytest.mark.parametrize("T,k,E", [(14000, 10, 512), (131072, 1, 7), (131073, 1, 40), (9000, 9, 4000), (300000, 3, 64)])
+def test_sort_of_long_batches(T, k, E):
+    """More chunks than a block adds up itself; against torch's stable sort."""
+    g = torch.Generator().manual_seed(T)
+    idx = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32)
+    ws = space(T, k, E)
+    got = moe.sort_pairs(idx.cuda(), E, ws)
+    flat = idx.view(-1).long()
+    key, order = torch.where(flat >= 0, flat, E).sort(stable=True)
+    kept = int((flat >= 0).sum())
+    row_of = torch.full((T * k,), -1, dtype=torch.int32)
+    row_of[order[:kept]] = torch.arange(kept, dtype=torch.int32)
+    src = torch.full((T * k,), -1, dtype=torch.int32)
+    src[:kept] = (order[:kept] // k).to(torch.int32)
+    counts = torch.bincount(key, minlength=E + 1)[:E]
+    assert torch.equal(got["counts"].cpu().long(), counts) and int(got["offsets"][-1]) == kept
+    assert torch.equal(got["offsets"].cpu().long()[1:], counts.cumsum(0))
+    assert torch.equal(got["row_of"].cpu().view(-1), row_of) and torch.equal(got["src"].cpu(), src)
+    assert moe.read_device_error(ws) == 0
+
+
 def test_sort_of_extreme_routings():
     check_sort(torch.full((300, 7), -1, dtype=torch.int32), 9)           # every token padded: no row at all
     check_sort(torch.full((300, 7), 8, dtype=torch.int32), 9)            # one expert takes all, the same one in every slot
