@@ -7,23 +7,28 @@
 // byte for 32 values, read from tensor memory), so the codes go from HBM to shared memory by TMA and from
 // there to the MMA untouched; only the scale bytes are rearranged on the way.
 //
-//   tile    128 rows of a group (MMA M, one tensor-memory lane a row) x NC columns: NC features, or NC / 2
-//           gate and NC / 2 up rows of the same features, whose accumulators one thread holds side by side
+//   tile    128 weight rows (MMA M, one tensor-memory lane a row: 128 features, or 64 features' gate rows and
+//           their up rows) x up to NT = 192 or 96 rows of a group (MMA N, a multiple of 16). A group of 160
+//           rows is one tile, so its weights are read once and no MMA works on rows that are not there.
+//           (With the rows as M = 128 such a group was two tiles, one a quarter full: 171 us for 8192 tokens
+//           over 512 experts, 198 under the power limit, against 156 and 182.)
 //   stage   K = 256: 128 bytes of codes a row (one 128-byte swizzle row), four MMAs of K = 64
 //   scales  per 128 rows and K = 128 one 512-byte block, row r's four bytes at (r % 32) 16 + (r / 32) 4;
 //           tcgen05.cp puts it into 4 columns of all four lane quarters. An MMA reads bytes 0-1 or 2-3.
-//   TMEM    two accumulators of NC columns and a set of scale columns a stage in flight. With NC = 256 the
-//           accumulators (columns 0 and 208) share 48 columns, which leaves room for two sets: a
-//           tile's epilogue first reads the shared ones into registers and lets the next tile begin.
-//           (Two sets hold a stage until the one but last has finished, about 1000 cycles from issue to
-//           commit: no loss while a stage's MMAs take 512, but 555 cycles a stage of an NC = 64
-//           tile, whose MMAs take 128. Three sets and 80 shared columns: the next tile began
-//           2000 cycles after a tile's end instead of 600.)
-//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warp 2 a fence, warps 4-11 epilogue (two a lane quarter),
-//           warps 12 on scales.
+//   TMEM    384 columns of accumulators (two of 192 or four of 96) and a set of scale columns a stage
+//   roles   one CTA an SM, persistent: warp 0 TMA, warp 1 MMA, warp 2 a fence, warps 4-11 epilogue (four warps a
+//           tile, in turn), warps 12 on scales.
+//
+// What bounds it, gate/up of 8192 tokens over 512 experts (K = 2048, N = 512): the 660 MB of weights, codes and
+// scales and 84 MB of results take 113 us of HBM time, the kernel 130 at the full clock; run back to back
+// it meets the power limit (1.44 GHz). Short groups are bound by the weights' bytes alone, single tokens by
+// the chain from launch to the last tile.
 //
 // Tiles are dealt round-robin with a group's row tiles innermost, so a weight tile is read from HBM once and
-// by the group's other row tiles from L2. Every wait is bounded and reports MOE_ERR_TIMEOUT.
+// by the group's other row tiles from L2. Every wait on a barrier in shared memory is bounded and reports
+// MOE_ERR_TIMEOUT.
+#include <type_traits>
+
 #include "block.cuh"
 #include "tc.cuh"
 
@@ -31,43 +36,44 @@ namespace moe {
 
 namespace {
 
-constexpr int kMxRows = 128;     // rows of a tile
-constexpr int kMxBoxRows = 32;   // rows of one TMA box of A: a short tile loads only the boxes it has rows in
+constexpr int kMxRows = 128;     // weight rows of a tile
+constexpr int kMxBox = 32;       // rows of one TMA box of the group's rows: a short tile loads only those it has
 constexpr int kMxStageK = 256;   // K of a stage
 constexpr int kMxRowBytes = kMxStageK / 2;
 constexpr int kMxTileCache = 128;  // tiles whose place is worked out once, in the prologue
+constexpr int kMxAccCols = 384;    // tensor memory columns of the accumulators, the scales behind them
 
-template <int NC>
-struct MxSmem {
-  static constexpr int kA = kMxRows * kMxRowBytes, kB = NC * kMxRowBytes;
-  static constexpr int kRowBlocks = (NC + 127) / 128;               // 128-row scale blocks of B
-  static constexpr int kSfA = 2 * 512, kSfB = 2 * kRowBlocks * 512;  // two K = 128 blocks a stage
-  static constexpr int kStage = kA + kB + kSfA + kSfB;
-  static constexpr int kStages = NC == 256 ? 4 : 6;
+// NT: rows of a group in a tile, at most
+template <int NT>
+struct MxCfg {
+  static constexpr int kRowBlocks = (NT + 127) / 128;  // 128-row scale blocks of the group's rows
+  static constexpr int kW = kMxRows * kMxRowBytes, kT = NT * kMxRowBytes;
+  static constexpr int kSfW = 2 * 512, kSfT = 2 * kRowBlocks * 512;  // two K = 128 blocks
+  static constexpr int kStage = kW + kT + kSfW + kSfT;
+  static constexpr int kStages = NT == 96 ? 6 : 4;
   static constexpr int kScaleWarps = kStages / 2, kThreads = 32 * (12 + kScaleWarps);
-  // tensor memory: column of the second accumulator, of the scales, columns and number of the scale sets
-  static constexpr int kAcc1 = NC == 256 ? 208 : NC, kSf = kAcc1 + NC, kSfCols = 8 + 8 * kRowBlocks;
-  static constexpr int kSfSets = NC == 256 ? 2 : kStages;
-  static constexpr int kOver = NC - kAcc1;  // columns that both accumulators use
-  static_assert(kSf + kSfSets * kSfCols <= 512 && kOver % 16 == 0, "tensor memory");
+  static constexpr int kAccs = kMxAccCols / NT, kSfCols = 8 + 8 * kRowBlocks;
+  static constexpr int kNumBars = 3 * kStages + 2 * kAccs;
+  // shared memory behind the stages: barriers, tiles, gate / up values on their way between lane quarters
+  // ([pair of warps][buffer][direction][8 columns][32 lanes] fp32), tiles before each group
   static constexpr int kBar = kStages * kStage;
-  static constexpr int kNumBars = 3 * kStages + 5;
   static constexpr int kTiles = kBar + (kNumBars * 8 + 16 + 15) / 16 * 16;
-  static constexpr int kPrefix = kTiles + kMxTileCache * 16;
-  static constexpr int bytes(int E) { return kPrefix + (E + 1) * 4 + 1024; }
+  static constexpr int kSwap = kTiles + kMxTileCache * 16;
+  static constexpr int smem(int E, bool up) { return kSwap + (up ? 4 * 2 * 2 * 1024 : 0) + (E + 1) * 4 + 1024; }
   static_assert(kStage % 1024 == 0, "stages start on swizzle atoms");
+  static_assert(kMxAccCols + kStages * kSfCols <= 512, "tensor memory");
 };
 
 struct MxArgs {
   const int32_t *offsets;
   const uint8_t *a_scales, *w_scales, *up_scales;
   void *out;
-  int out_type, n_rows, K, N, E, n_tiles_n;
+  int out_type, n_rows, K, N, E, m_tiles;
   Ctrl *ctrl;
 };
 
 struct alignas(16) MxTile {
-  int group, row0, rows, n0;
+  int group, tok0, toks, m0;  // toks rows from tok0; features from m0
 };
 
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
@@ -112,25 +118,28 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, int type) {
-  if (type == MOE_BF16) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&b);
-  }
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
+template <bool BF>
+__device__ __forceinline__ uint16_t cvt16(float v) {
+  if constexpr (BF) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  else return __half_as_ushort(__float2half_rn(v));
 }
-// A lane's 32 bytes of its own row: a warp's store touches 32 lines whatever its width, and their number is
-// what the epilogue's stores cost, so one 32-byte store beats two of 16.
-__device__ __forceinline__ void store32(void *p, const uint32_t y[8], bool aligned32) {
-  if (aligned32) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]),
-                 "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                 : "memory");
-    return;
+// n of a lane's values of C consecutive rows to those rows, N values apart. The type is known at compile time and a
+// whole chunk is stored without tests: with both decided value by value a store took 70 cycles.
+template <bool BF, int C>
+__device__ __forceinline__ void store_rows(uint16_t *o, int N, const float y[C], int n) {
+  if (n >= C) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      *o = cvt16<BF>(y[j]);
+      o += N;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if (j < n) *o = cvt16<BF>(y[j]);
+      o += N;
+    }
   }
-  static_cast<uint4 *>(p)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  static_cast<uint4 *>(p)[1] = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
 __device__ __forceinline__ void mx_timeout(Ctrl *ctrl, int where) { set_device_error(ctrl, MOE_ERR_TIMEOUT, where); }
@@ -149,19 +158,19 @@ __device__ __forceinline__ int2 mx_group(const MxArgs &a, int g) {
 // parity wait that skipped a use would take the phase before the last for the last. Where K % 512 = 0
 // a pair is 16 bytes a row, otherwise each stage's 8 are read apart. Four rows 32 apart are 16
 // consecutive bytes of a scale block.
-template <int NC, bool UP, class TileAt>
+template <bool UP, int NT, class TileAt>
 struct MxScales {
-  static constexpr int kRows = 4 + NC / 32, kFeat = UP ? NC / 2 : NC;
+  static constexpr int kRows = 4 + NT / 32, kFeat = UP ? 64 : 128;
   const MxArgs &a;
   const TileAt &tile_at;
   const int n_my, nk, lane;
 
   __device__ __forceinline__ const uint8_t *row(const MxTile &t, int i) const {
     const int pitch = a.K / 32;
-    if (i < 4) return a.a_scales + (size_t)(t.row0 + min(lane + 32 * i, t.rows - 1)) * pitch;
-    const int r = lane + 32 * (i - 4);
+    if (i >= 4) return a.a_scales + (size_t)(t.tok0 + min(lane + 32 * (i - 4), t.toks - 1)) * pitch;
+    const int r = lane + 32 * i;
     const bool up = UP && r >= kFeat;
-    const int wr = min(t.group * a.N + t.n0 + (up ? r - kFeat : r), a.E * a.N - 1);
+    const int wr = min(t.group * a.N + t.m0 + (up ? r - kFeat : r), a.E * a.N - 1);
     return (up ? a.up_scales : a.w_scales) + (size_t)wr * pitch;
   }
 
@@ -186,7 +195,7 @@ struct MxScales {
   __device__ __forceinline__ void run(int w, const Put &put) const {
     const int total = n_my * nk;
     const bool wide = a.K % 512 == 0;  // nk is even, a pair is in one tile
-    for (int g = 2 * w; g < total; g += MxSmem<NC>::kStages) {
+    for (int g = 2 * w; g < total; g += MxCfg<NT>::kStages) {
       uint32_t v[2][2][kRows];  // [stage][word]
       const bool two = g + 1 < total;
       if (wide) {
@@ -194,6 +203,7 @@ struct MxScales {
         const int at = 8 * (g % nk);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
+          if (i > 4 && 32 * (i - 4) >= t.toks) break;
           const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row(t, i) + at));
           v[0][0][i] = x.x;
           v[0][1][i] = x.y;
@@ -207,6 +217,7 @@ struct MxScales {
           const MxTile t = tile_at((g + h) / nk);
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
+            if (i > 4 && 32 * (i - 4) >= t.toks) break;
             uint32_t x[2];
             load8(row(t, i), (g + h) % nk, x);
             v[h][0][i] = x[0];
@@ -219,26 +230,25 @@ struct MxScales {
   }
 };
 
-template <int NC, bool UP>
-__global__ void __launch_bounds__(MxSmem<NC>::kThreads, 1)
+template <bool UP, bool BF, int NT>
+__global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
 mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_u, const MxArgs args) {
-  using S = MxSmem<NC>;
-  constexpr int kStages = S::kStages, kFeat = UP ? NC / 2 : NC;
+  using S = MxCfg<NT>;
+  constexpr int kStages = S::kStages, kAccs = S::kAccs, kFeat = UP ? 64 : 128;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *gbase = smem_raw + (base - smem_u32(smem_raw));
-  auto st_a = [&](int s) { return base + s * S::kStage; };
-  auto st_b = [&](int s) { return base + s * S::kStage + S::kA; };
-  auto st_sf = [&](int s) { return base + s * S::kStage + S::kA + S::kB; };
+  auto st_w = [&](int s) { return base + s * S::kStage; };
+  auto st_t = [&](int s) { return base + s * S::kStage + S::kW; };
+  auto st_sf = [&](int s) { return base + s * S::kStage + S::kW + S::kT; };
   auto full = [&](int s) { return base + S::kBar + 8u * s; };
   auto empty = [&](int s) { return base + S::kBar + 8u * (kStages + s); };
-  auto acc_full = [&](int b) { return base + S::kBar + 8u * (2 * kStages + b); };
-  auto acc_empty = [&](int b) { return base + S::kBar + 8u * (2 * kStages + 2 + b); };
-  const uint32_t acc_over = base + S::kBar + 8u * (2 * kStages + 4);  // the shared columns are read
-  auto sf_in = [&](int s) { return base + S::kBar + 8u * (2 * kStages + 5 + s); };
+  auto sf_in = [&](int s) { return base + S::kBar + 8u * (2 * kStages + s); };
+  auto acc_full = [&](int b) { return base + S::kBar + 8u * (3 * kStages + b); };
+  auto acc_empty = [&](int b) { return base + S::kBar + 8u * (3 * kStages + kAccs + b); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + S::kBar + S::kNumBars * 8);
-  int32_t *s_pref = reinterpret_cast<int32_t *>(gbase + S::kPrefix);  // [E + 1] tiles before a group
+  int32_t *s_pref = reinterpret_cast<int32_t *>(gbase + S::kSwap + (UP ? 4 * 2 * 2 * 1024 : 0));  // [E + 1]
   __shared__ int32_t s_warp[S::kThreads / 32];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -249,11 +259,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       mbar_init(sf_in(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 8);
+      mbar_init(acc_empty(b), 4);
     }
-    mbar_init(acc_over, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -280,7 +289,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       if (i >= per || g >= args.E) continue;
       const int s0 = min(max(at[i], 0), args.n_rows), s1 = min(max(at[i + 1], s0), args.n_rows);
       if (s0 != at[i] || s1 != at[i + 1] || (g == 0 && s0 != 0)) set_device_error(ctrl, MOE_ERR_DEVICE_CHECK, g);
-      at[i] = (s1 - s0 + kMxRows - 1) / kMxRows * args.n_tiles_n;
+      at[i] = (s1 - s0 + NT - 1) / NT * args.m_tiles;
       mine += at[i];
     }
     int incl = mine;
@@ -317,13 +326,14 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       if (s_pref[mid] <= ti) lo = mid;
       else hi = mid - 1;
     }
-    const int mt = (s_pref[lo + 1] - s_pref[lo]) / args.n_tiles_n, local = ti - s_pref[lo];
+    const int tt = (s_pref[lo + 1] - s_pref[lo]) / args.m_tiles, local = ti - s_pref[lo];
     const int2 r = mx_group(args, lo);
+    const int size = ((r.y - r.x + tt - 1) / tt + 15) & ~15;
     MxTile t;
     t.group = lo;
-    t.row0 = r.x + (local % mt) * kMxRows;
-    t.rows = min(kMxRows, r.y - t.row0);
-    t.n0 = (local / mt) * kFeat;
+    t.tok0 = r.x + (local % tt) * size;
+    t.toks = min(size, r.y - t.tok0);
+    t.m0 = (local / tt) * kFeat;
     return t;
   };
   MxTile *s_tiles = reinterpret_cast<MxTile *>(gbase + S::kTiles);
@@ -331,9 +341,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   __syncthreads();
   auto uniform_tile = [&](MxTile t) {
     t.group = __shfl_sync(0xffffffffu, t.group, 0);
-    t.row0 = __shfl_sync(0xffffffffu, t.row0, 0);
-    t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
-    t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+    t.tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
+    t.toks = __shfl_sync(0xffffffffu, t.toks, 0);
+    t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);
     return t;
   };
   auto tile_at = [&](int tl) { return tl < kMxTileCache ? s_tiles[tl] : find_tile(tl); };
@@ -344,8 +354,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     int g = 0;
     for (int tl = 0; tl < n_my && ok; ++tl) {
       const MxTile t = uniform_tile(tile_at(tl));
-      const int nbox = (t.rows + kMxBoxRows - 1) / kMxBoxRows, wrow = t.group * args.N + t.n0;
-      const uint32_t tx = (uint32_t)(nbox * kMxBoxRows + NC) * kMxRowBytes;
+      const int nbox = (t.toks + kMxBox - 1) / kMxBox, wrow = t.group * args.N + t.m0;
+      const uint32_t tx = (uint32_t)(nbox * kMxBox + kMxRows) * kMxRowBytes;
       for (int ks = 0; ks < nk; ++ks, ++g) {
         const int s = g % kStages;
         if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
@@ -355,10 +365,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         }
         if (elect_one()) {
           mbar_arrive_expect_tx(full(s), tx);
-          tma_load_2d(st_b(s), &tm_w, ks * kMxRowBytes, wrow, full(s));
-          if (UP) tma_load_2d(st_b(s) + kFeat * kMxRowBytes, &tm_u, ks * kMxRowBytes, wrow, full(s));
+          tma_load_2d(st_w(s), &tm_w, ks * kMxRowBytes, wrow, full(s));
+          if (UP) tma_load_2d(st_w(s) + kFeat * kMxRowBytes, &tm_u, ks * kMxRowBytes, wrow, full(s));
           for (int b = 0; b < nbox; ++b)
-            tma_load_2d(st_a(s) + b * kMxBoxRows * kMxRowBytes, &tm_a, ks * kMxRowBytes, t.row0 + b * kMxBoxRows, full(s));
+            tma_load_2d(st_t(s) + b * kMxBox * kMxRowBytes, &tm_a, ks * kMxRowBytes, t.tok0 + b * kMxBox, full(s));
         }
         __syncwarp();
       }
@@ -367,50 +377,43 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     for (int j = max(0, g - kStages); j < g; ++j) (void)mbar_wait(full(j % kStages), (uint32_t)(j / kStages) & 1u);
   } else if (warp == 1) {
     // ------------------------------------------------ MMA
-    const uint32_t id0 = idesc_mxf4(NC, 0), id2 = idesc_mxf4(NC, 2);
     bool ok = true;
     int g = 0;
     for (int tl = 0; tl < n_my && ok; ++tl) {
-      const int b = tl & 1;
-      const bool go = mbar_wait(acc_empty(b), (((uint32_t)tl >> 1) & 1u) ^ 1u) &&
-                      (S::kOver == 0 || tl == 0 || mbar_wait(acc_over, (uint32_t)(tl - 1) & 1u));
-      if (!__all_sync(0xffffffffu, go)) {
+      const int b = tl % kAccs, toks = __shfl_sync(0xffffffffu, tile_at(tl).toks, 0);
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_empty(b), ((uint32_t)(tl / kAccs) & 1u) ^ 1u))) {
         if (lane == 0) mx_timeout(ctrl, 42);
         break;
       }
       tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(b * S::kAcc1);
+      const uint32_t d = tmem + (uint32_t)(b * NT);
+      const int N = (toks + 15) & ~15;
+      const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
       for (int ks = 0; ks < nk; ++ks, ++g) {
         const int s = g % kStages;
-        // the scale columns of stage g were read by the MMAs of stage g - kSfSets; with a set a stage
-        // the stage's own slot says so
-        constexpr int kBack = S::kSfSets;
-        const bool in = mbar_wait(full(s), (uint32_t)(g / kStages) & 1u) &&
-                        (kBack == kStages || g < kBack ||
-                         mbar_wait(empty((g - kBack) % kStages), (uint32_t)((g - kBack) / kStages) & 1u));
-        if (!__all_sync(0xffffffffu, in)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full(s), (uint32_t)(g / kStages) & 1u))) {
           if (lane == 0) mx_timeout(ctrl, 43);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sf = tmem + (uint32_t)(S::kSf + g % kBack * S::kSfCols);
-        const uint64_t dsf = plain_desc(st_sf(s)), da = sw128_desc(st_a(s)), db = sw128_desc(st_b(s));
+        // the slot's own set of scale columns: its last readers were done when the slot was filled again
+        const uint32_t sf = tmem + (uint32_t)(kMxAccCols + s * S::kSfCols);
+        const uint64_t dsf = plain_desc(st_sf(s)), da = sw128_desc(st_w(s)), db = sw128_desc(st_t(s));
         const int steps = (args.K - ks * kMxStageK) / 64;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             tc_cp_scales(sf + 4u * j, dsf + (uint64_t)((512 * j) >> 4));
-#pragma unroll
-            for (int r = 0; r < S::kRowBlocks; ++r)
-              tc_cp_scales(sf + 8u + 8u * j + 4u * r,
-                           dsf + (uint64_t)((S::kSfA + 512 * (j * S::kRowBlocks + r)) >> 4));
+            tc_cp_scales(sf + 8u + 4u * S::kRowBlocks * j, dsf + (uint64_t)((S::kSfW + 512 * S::kRowBlocks * j) >> 4));
+            if (S::kRowBlocks > 1 && toks > 128)
+              tc_cp_scales(sf + 12u + 8u * j, dsf + (uint64_t)((S::kSfW + 1024 * j + 512) >> 4));
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (q < steps)
               tc_mma_mxf4(d, da + (uint64_t)((32 * q) >> 4), db + (uint64_t)((32 * q) >> 4), (q & 1) ? id2 : id0,
-                          sf + 4u * (q >> 1), sf + 8u + 8u * (q >> 1), (ks | q) ? 1u : 0u);
+                          sf + 4u * (q >> 1), sf + 8u + 4u * S::kRowBlocks * (q >> 1), (ks | q) ? 1u : 0u);
           tc_commit(empty(s));
           if (ks == nk - 1) tc_commit(acc_full(b));
         }
@@ -437,69 +440,66 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       }
     }
   } else if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------ epilogue: a lane quarter and every other 16 features
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    // ------------------------------------------------ epilogue: four warps, a lane quarter each, every other tile
+    const int q = warp & 3, who = (warp - 4) >> 2;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-    constexpr int kChunks = kFeat / 16, kIt = kFeat / 32;
-    static_assert(S::kOver <= 48, "the shared columns are each warp's first chunk or two");
-    const bool out32 = ((uintptr_t)args.out & 31u) == 0;
-    for (int tl = 0; tl < n_my; ++tl) {
+    uint16_t *out = static_cast<uint16_t *>(args.out);
+    // With gate and up, quarters 0 and 1 hold 64 features' gate rows, 2 and 3 their up rows. Of 16 columns the gate
+    // warp finishes the first 8 and the up warp the others; each hands its partner the 8 values that
+    // the partner lacks. Buffers alternate, so one barrier of the pair an exchange is enough.
+    const int pair = (q & 1) + 2 * who;
+    float *swap = reinterpret_cast<float *>(gbase + S::kSwap) + pair * 4 * 256;
+    int turn = 0;
+    bool ok = true;  // after a time-out a warp goes on through its partner's barriers, without waiting again
+    for (int tl = who; tl < n_my; tl += 2) {
       const MxTile t = tile_at(tl);
-      const int b = tl & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(acc_full(b), ((uint32_t)tl >> 1) & 1u))) {
+      const int b = tl % kAccs;
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(acc_full(b), (uint32_t)(tl / kAccs) & 1u))) {
         if (lane == 0) mx_timeout(ctrl, 44);
-        break;
+        ok = false;
       }
       tc_fence_after();
-      const uint32_t acc = tmem + lane_base + (uint32_t)(b * S::kAcc1);
-      const int r = 32 * q + lane;
-      uint8_t *op = static_cast<uint8_t *>(args.out) + ((size_t)(t.row0 + r) * args.N + t.n0) * 2;
-      // from the end that the other accumulator shares, so that those columns are read first
-      auto feat = [&](int it) { return 16 * (b ? 2 * it + half : kChunks - 1 - 2 * it - half); };
-      uint32_t v[2][16], u[2][16];
-      auto load = [&](int it, int p) {
-        mx_ld16(acc + feat(it), v[p]);
-        if (UP) mx_ld16(acc + kFeat + feat(it), u[p]);
-      };
-      const bool any = 32 * q < t.rows;  // a quarter without rows has nothing to read
-      if (any) {
-        load(0, 0);
-        if (kIt > 1) load(1, 1);
-        tmem_ld_wait16(v[0]);
-        tmem_ld_wait16(v[1]);
-        if (UP) {
-          tmem_ld_wait16(u[0]);
-          tmem_ld_wait16(u[1]);
-        }
-      }
-      if (S::kOver) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_over);
-      }
-#pragma unroll 1
-      for (int it0 = 0; any && it0 < kIt; it0 += 2) {
+      const uint32_t acc = tmem + lane_base + (uint32_t)(b * NT);
+      const int f = t.m0 + 32 * (UP ? q & 1 : q) + lane;
+      uint16_t *op = out + (size_t)t.tok0 * args.N + f;
+      if (UP || f < args.N) {  // a whole warp's rows are there or none are: N % 64 = 0
+        uint32_t v[2][16];
+        auto finish = [&](int c, const uint32_t x[16]) {
+          uint16_t *o = op + (size_t)c * args.N;
+          const int left = ok ? t.toks - c : 0;
+          if constexpr (UP) {
+            const bool up_warp = q >= 2;
+            float *w = swap + turn * 512 + (up_warp ? 256 : 0), *r = swap + turn * 512 + (up_warp ? 0 : 256);
+            turn ^= 1;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int it = it0 + p;
-          if (it >= kIt) break;
-          const int f = feat(it);
-          if (it >= 2) {
-            tmem_ld_wait16(v[p]);
-            if (UP) tmem_ld_wait16(u[p]);
-          }
-          uint32_t y[8];
+            for (int j = 0; j < 8; ++j) w[32 * j + lane] = __uint_as_float(up_warp ? x[j] : x[8 + j]);
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+            float y[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float a = __uint_as_float(v[p][2 * j]), c = __uint_as_float(v[p][2 * j + 1]);
-            if (UP) {
-              a = __fdividef(a, 1.0f + __expf(-a)) * __uint_as_float(u[p][2 * j]);
-              c = __fdividef(c, 1.0f + __expf(-c)) * __uint_as_float(u[p][2 * j + 1]);
+            for (int j = 0; j < 8; ++j) {
+              const float other = r[32 * j + lane], own = __uint_as_float(up_warp ? x[8 + j] : x[j]);
+              const float gate = up_warp ? other : own, upv = up_warp ? own : other;
+              y[j] = __fdividef(gate, 1.0f + __expf(-gate)) * upv;
             }
-            y[j] = pack16(a, c, args.out_type);
+            store_rows<BF, 8>(up_warp ? o + 8 * (size_t)args.N : o, args.N, y, up_warp ? left - 8 : left);
+          } else {
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(x[j]);
+            store_rows<BF, 16>(o, args.N, y, left);
           }
-          if (it + 2 < kIt) load(it + 2, p);
-          if (r < t.rows && t.n0 + f < args.N) store32(op + 2 * f, y, out32);
+        };
+        mx_ld16(acc, v[0]);
+#pragma unroll 1
+        for (int c = 0; c < t.toks; c += 32) {  // the next 16 columns are on their way while 16 are stored
+          tmem_ld_wait16(v[0]);
+          if (c + 16 < t.toks) mx_ld16(acc + c + 16, v[1]);
+          finish(c, v[0]);
+          if (c + 16 < t.toks) {
+            tmem_ld_wait16(v[1]);
+            if (c + 32 < t.toks) mx_ld16(acc + c + 32, v[0]);
+            finish(c + 16, v[1]);
+          }
         }
       }
       tc_fence_before();
@@ -514,8 +514,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       store8(args.out, args.out_type, 8 * i, z);
   } else if (warp >= 12) {
     // ------------------------------------------------ scales
-    const MxScales<NC, UP, decltype(tile_at)> scales{args, tile_at, n_my, nk, lane};
-    auto put = [&](int g, const uint32_t x[2][4 + NC / 32]) {  // stage g's scales of all rows
+    const MxScales<UP, NT, decltype(tile_at)> scales{args, tile_at, n_my, nk, lane};
+    auto put = [&](int g, const uint32_t x[2][4 + NT / 32]) {  // stage g's scales of all rows
       const int s = g % kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ((uint32_t)(g / kStages) & 1u) ^ 1u))) {
         if (lane == 0) mx_timeout(ctrl, 45);
@@ -525,13 +525,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         sf[32 * j] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
-        uint4 *sb = sf + S::kSfA / 16 + 32 * j * S::kRowBlocks;
-        if constexpr (NC < 128) {
-          *reinterpret_cast<uint2 *>(sb) = make_uint2(x[j][4], x[j][5]);
+        uint4 *sb = sf + S::kSfW / 16 + 32 * S::kRowBlocks * j;
+        if constexpr (NT == 96) {
+          sb[0] = make_uint4(x[j][4], x[j][5], x[j][6], 0u);
         } else {
-#pragma unroll
-          for (int r = 0; r < S::kRowBlocks; ++r)
-            sb[32 * r] = make_uint4(x[j][4 + 4 * r], x[j][5 + 4 * r], x[j][6 + 4 * r], x[j][7 + 4 * r]);
+          sb[0] = make_uint4(x[j][4], x[j][5], x[j][6], x[j][7]);
+          *reinterpret_cast<uint2 *>(sb + 32) = make_uint2(x[j][8], x[j][9]);
         }
       }
       __syncwarp();
@@ -548,53 +547,49 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   }
 }
 
-template <int NC, bool UP>
-cudaError_t launch_nc(const Mx4ProductArgs &p, cudaStream_t s) {
-  constexpr int kFeat = UP ? NC / 2 : NC;
+template <bool UP, bool BF, int NT>
+cudaError_t launch_tiles(const Mx4ProductArgs &p, cudaStream_t s) {
+  constexpr int kFeat = UP ? 64 : 128;
   const uint64_t kb = (uint64_t)p.K / 2, wr = (uint64_t)p.E * p.N;
   CUtensorMap ta, tw, tu;
   auto map = [&](CUtensorMap *m, const uint8_t *ptr, uint64_t rows, int box) {
     return encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, kb, rows, kMxRowBytes, box,
                                 CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  if (!map(&ta, p.a_codes, p.n_rows, kMxBoxRows) || !map(&tw, p.w_codes, wr, kFeat) ||
-      !map(&tu, UP ? p.up_codes : p.w_codes, wr, kFeat))
-    return cudaErrorInvalidValue;
-  const int nt = (p.N + kFeat - 1) / kFeat;
-  const MxArgs a{p.offsets, p.a_scales, p.w_scales, p.up_scales, p.out, p.out_type, p.n_rows, p.K, p.N, p.E, nt, p.ctrl};
+  if (!map(&ta, p.a_codes, p.n_rows, kMxBox) || !map(&tw, p.w_codes, wr, kFeat)) return cudaErrorInvalidValue;
+  if (!UP) tu = tw;
+  else if (!map(&tu, p.up_codes, wr, kFeat)) return cudaErrorInvalidValue;
+  const int mt = (p.N + kFeat - 1) / kFeat;
+  const MxArgs a{p.offsets, p.a_scales, p.w_scales, p.up_scales, p.out, p.out_type, p.n_rows, p.K, p.N, p.E, mt, p.ctrl};
   const int live = p.E < p.n_rows ? p.E : p.n_rows;  // at most: every live group's last tile is partial
-  const long long most = ((long long)p.n_rows / kMxRows + live) * nt;
+  const long long most = ((long long)p.n_rows / NT + live) * mt;
   const int grid = (int)(most < num_sms() ? most : num_sms());
-  const cudaError_t e = smem_limit_once(mx4_product_kernel<NC, UP>, MxSmem<NC>::bytes(kMaxE));
+  const cudaError_t e = smem_limit_once(mx4_product_kernel<UP, BF, NT>, MxCfg<NT>::smem(kMaxE, UP));
   if (e != cudaSuccess) return e;
   KTimer kt_(KID_MX4_PRODUCT, s);
   // A short product begins while its predecessor ends (four tokens: 0.5 us). A long one gains nothing, and with
   // its blocks waiting beside the quantiser's the two took 173-180 us for 8192 tokens, not 172.
   if (p.n_rows <= 4096)
-    return launch_pdl(mx4_product_kernel<NC, UP>, dim3(grid), dim3(MxSmem<NC>::kThreads), MxSmem<NC>::bytes(p.E), s, ta,
-                      tw, tu, a);
-  mx4_product_kernel<NC, UP><<<grid, MxSmem<NC>::kThreads, MxSmem<NC>::bytes(p.E), s>>>(ta, tw, tu, a);
+    return launch_pdl(mx4_product_kernel<UP, BF, NT>, dim3(grid), dim3(MxCfg<NT>::kThreads), MxCfg<NT>::smem(p.E, UP), s, ta, tw, tu, a);
+  mx4_product_kernel<UP, BF, NT><<<grid, MxCfg<NT>::kThreads, MxCfg<NT>::smem(p.E, UP), s>>>(ta, tw, tu, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_product(const Mx4ProductArgs &p, cudaStream_t s) {
-  // Columns of a tile. 256: fewest bytes from L2 and the MMAs' best rate, for groups of many rows (8192 tokens
-  // over 512 experts, 160 rows each: 171 us with the quantiser, 189 with 128). 128: less left over at the
-  // end and an epilogue of two accumulators, for the others (2048 tokens, down, 40 rows each: 68.5 us, 70.5 with
-  // 256; four tokens: 21.0 us cold, 22.6). 64: more SMs at work where 128 leaves some idle (four groups of
-  // 64 rows, K = 4096, N = 1024: 14.4 us, 16.0 with 128, 18.5 with 256).
-  const bool up = p.up_codes != nullptr;
-  const int live = p.E < p.n_rows ? p.E : p.n_rows;
-  auto tiles = [&](int nc) {  // at most: every live group's last tile is partial
-    const int feat = up ? nc / 2 : nc;
-    return ((long long)p.n_rows / kMxRows + live) * ((p.N + feat - 1) / feat);
+  // Rows of a tile: 192 where groups are long (8192 tokens over 512 experts, 160 rows each, with the quantiser:
+  // 156 us, 185 with 96), else 96: a stage is smaller and more are in flight, and four accumulators leave
+  // short tiles' epilogues behind (2048 tokens, down, 40 rows each: 67.8 us, 72.2 with 192; ten rows of
+  // one token: 12.3 us cold, 13.8).
+  const bool long_groups = p.n_rows > 80ll * p.E;
+  auto run = [&](auto up, auto bf) {
+    return long_groups ? launch_tiles<up.value, bf.value, 192>(p, s) : launch_tiles<up.value, bf.value, 96>(p, s);
   };
-  if (tiles(256) >= 4ll * num_sms() && p.n_rows >= 64ll * p.E)
-    return up ? launch_nc<256, true>(p, s) : launch_nc<256, false>(p, s);
-  if (tiles(128) >= num_sms()) return up ? launch_nc<128, true>(p, s) : launch_nc<128, false>(p, s);
-  return up ? launch_nc<64, true>(p, s) : launch_nc<64, false>(p, s);
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  if (p.out_type == MOE_BF16) return p.up_codes ? run(yes, yes) : run(no, yes);
+  return p.up_codes ? run(yes, no) : run(no, no);
 }
 
 }  // namespace moe

@@ -109,7 +109,8 @@ def test_product_sizes(K, N, up):
 
 
 @pytest.mark.parametrize("up", [False, True])
-@pytest.mark.parametrize("sizes", [[1], [0, 1], [1, 0, 0], [8, 16, 32, 64], [127, 128, 129], [255, 256, 257], [15, 1, 33, 0, 500],
+@pytest.mark.parametrize("sizes", [[1], [0, 1], [1, 0, 0], [8, 16, 32, 64], [127, 128, 129], [255, 256, 257], [15, 1, 33, 0, 500], [192, 193, 191],
+                                   [97, 96, 95, 1, 0], [385, 577, 15], [300, 0, 0, 0, 10], [80, 81], [176, 1, 353],
                                    [0, 0, 0]])
 def test_product_groups(sizes, up):
     if sum(sizes):
