@@ -82,7 +82,7 @@ __device__ __forceinline__ void store_raw8(void *base, int type, size_t i, const
 constexpr int kAny = -1, k16 = 4;
 template <int KT>
 __device__ __forceinline__ int known_type(int type) {
-  if constexpr (KT == kF32Wide) return kF32Wide;
+  if constexpr (KT == kF32Wide || KT == MOE_F16 || KT == MOE_BF16) return KT;
   else if constexpr (KT == k16) return type == MOE_BF16 ? MOE_BF16 : MOE_F16;
   else return type;
 }

@@ -285,32 +285,37 @@ collect_grad_kernel(const void *__restrict__ dy, int in_type, const void *rows, 
     float dot = 0.0f;
     if (r >= 0 && r < P) {
       const float wp = w ? w[p] : 1.0f;
-      for (int c0 = lane; c0 < H8; c0 += 32 * 4) {
+      const size_t at_t = (size_t)t * H, at_r = (size_t)r * H;
+      auto chunk = [&](int c, const Raw8 &g, const Raw8 &v) {
+        float a[8], b[8];
+        raw8_to_float(g, dy_type, a);
+        if (d_w) {
+          raw8_to_float(v, type, b);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dot = fmaf(a[q], b[q], dot);
+        }
+        if (d_rows) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) a[q] *= wp;
+          store8(d_rows, type, at_r + 8 * c, a);
+        }
+      };
+      int c0 = lane;
+      for (; c0 + 96 < H8; c0 += 128) {  // four chunks of each in flight
         Raw8 g[4], v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int c = c0 + 32 * u;
-          if (c >= H8) continue;
-          g[u] = load_raw8(dy, dy_type, ((size_t)t * H8 + c) * 8);
-          if (d_w) v[u] = load_raw8(rows, type, ((size_t)r * H8 + c) * 8);
+          g[u] = load_raw8(dy, dy_type, at_t + 8 * (c0 + 32 * u));
+          if (d_w) v[u] = load_raw8(rows, type, at_r + 8 * (c0 + 32 * u));
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = c0 + 32 * u;
-          if (c >= H8) continue;
-          float a[8], b[8];
-          raw8_to_float(g[u], dy_type, a);
-          if (d_w) {
-            raw8_to_float(v[u], type, b);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dot = fmaf(a[q], b[q], dot);
-          }
-          if (d_rows) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) a[q] *= wp;
-            store8(d_rows, type, ((size_t)r * H8 + c) * 8, a);
-          }
-        }
+        for (int u = 0; u < 4; ++u) chunk(c0 + 32 * u, g[u], v[u]);
+      }
+      for (; c0 < H8; c0 += 32) {
+        Raw8 v;
+        const Raw8 g = load_raw8(dy, dy_type, at_t + 8 * c0);
+        if (d_w) v = load_raw8(rows, type, at_r + 8 * c0);
+        chunk(c0, g, v);
       }
       dot = warp_sum(dot);
     }
@@ -366,17 +371,17 @@ cudaError_t launch_dispatch(const void *x, int type, int T, int k, int H, const 
                     H, row_of, kept, rows);
 }
 
-// calls f with what is known of two types at compile time
+// calls f with two types at compile time (fp32 that is not 32-byte aligned: with types told apart at run time)
 template <class F>
 cudaError_t by_types(int a, int b, const F &f) {
   using std::integral_constant;
   constexpr integral_constant<int, kAny> any{};
   constexpr integral_constant<int, kF32Wide> w{};
-  constexpr integral_constant<int, k16> n{};
-  const int ka = known_of(a), kb = known_of(b);
-  if (ka == kAny || kb == kAny) return f(any, any);
-  if (ka == kF32Wide) return kb == kF32Wide ? f(w, w) : f(w, n);
-  return kb == kF32Wide ? f(n, w) : f(n, n);
+  constexpr integral_constant<int, MOE_F16> h{};
+  constexpr integral_constant<int, MOE_BF16> n{};
+  if (a == MOE_F32 || b == MOE_F32) return f(any, any);
+  auto second = [&](auto x) { return b == kF32Wide ? f(x, w) : b == MOE_F16 ? f(x, h) : f(x, n); };
+  return a == kF32Wide ? second(w) : a == MOE_F16 ? second(h) : second(n);
 }
 
 cudaError_t launch_collect(const void *rows, int type, int T, int k, int H, const int32_t *row_of, const float *w,
@@ -388,7 +393,7 @@ cudaError_t launch_collect(const void *rows, int type, int T, int k, int H, cons
   const long long items = (long long)T * ((H / 8 + 32 * per - 1) / (32 * per));
   const bool wide = items >= 16ll * num_sms();
   return by_types(type, y_type, [&](auto r, auto o) {
-    constexpr int CH = r.value == k16 ? 4 : 2;
+    constexpr int CH = r.value == MOE_F16 || r.value == MOE_BF16 ? 4 : 2;
     if (wide)
       return launch_pdl(collect_kernel<CH, r.value, o.value>, dim3(warp_grid(items)), dim3(256), 0, s, rows, type, T, k, H,
                         row_of, w, residual, y, y_type);
