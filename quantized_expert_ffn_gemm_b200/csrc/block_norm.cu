@@ -528,19 +528,20 @@ __global__ void __launch_bounds__(512, 1) block_norm_grad_long_kernel(const Bloc
   }
 }
 
-// the blocks' partial sums added in a fixed order: 32 channels a block, 32 row groups, eight loads in flight
+// The blocks' partial sums added in a fixed order: 16 channels a block, 64 groups of rows, eight loads in flight.
+// The kernel is a few dependent loads long (5 us for 296 rows of 2 x 2048), so it is spread thin.
 __global__ void __launch_bounds__(1024) block_norm_gain_kernel(const BlockNormGradArgs a,
                                                               const float *__restrict__ part, int n) {
-  __shared__ float s[2][32][33];
-  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, h = blockIdx.x * 32 + lane;
+  __shared__ float s[2][64][17];
+  const int ch = threadIdx.x & 15, grp = threadIdx.x >> 4, h = blockIdx.x * 16 + ch;
   pdl_launch_dependents();
   pdl_wait();
   float v = 0.0f, x = 0.0f;
-  for (int i0 = grp; i0 < n; i0 += 32 * 4) {
+  for (int i0 = grp; i0 < n; i0 += 64 * 4) {
     float pv[4], px[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 32 * j;
+      const int i = i0 + 64 * j;
       pv[j] = i < n ? part[(size_t)i * 2 * a.H + h] : 0.0f;
       px[j] = i < n ? part[(size_t)i * 2 * a.H + a.H + h] : 0.0f;
     }
@@ -550,18 +551,19 @@ __global__ void __launch_bounds__(1024) block_norm_gain_kernel(const BlockNormGr
       x += px[j];
     }
   }
-  s[0][grp][lane] = v;
-  s[1][grp][lane] = x;
+  s[0][grp][ch] = v;
+  s[1][grp][ch] = x;
   __syncthreads();
-  // warp w adds the groups' sums of channel w (lane = group)
-  v = warp_sum(s[0][lane][grp]);
-  x = warp_sum(s[1][lane][grp]);
-  if (lane == 0) {
-    const int c = blockIdx.x * 32 + grp;
-    const float gate = a.gate_mode == MOE_GATE_CHANNEL ? a.gate[c] : 1.0f;
-    if (a.d_post_gain) a.d_post_gain[c] = gate * v;
-    if (a.d_gate && a.gate_mode == MOE_GATE_CHANNEL) a.d_gate[c] = (a.post_gain ? a.post_gain[c] : 1.0f) * v;
-    if (a.d_pre_gain) a.d_pre_gain[c] = x;
+  // a warp joins the groups of one channel's one sum
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 16 + (warp >> 1);
+  const float(*t)[17] = s[warp & 1];
+  const float sum = warp_sum(t[lane][warp >> 1] + t[lane + 32][warp >> 1]);
+  if (lane) return;
+  if (warp & 1) {
+    if (a.d_pre_gain) a.d_pre_gain[c] = sum;
+  } else {
+    if (a.d_post_gain) a.d_post_gain[c] = (a.gate_mode == MOE_GATE_CHANNEL ? a.gate[c] : 1.0f) * sum;
+    if (a.d_gate && a.gate_mode == MOE_GATE_CHANNEL) a.d_gate[c] = (a.post_gain ? a.post_gain[c] : 1.0f) * sum;
   }
 }
 
@@ -683,7 +685,7 @@ cudaError_t launch_block_norm_grad(const BlockNormGradArgs &args, float *scratch
   }
   if (e == cudaSuccess && sums) {
     KTimer kt_(KID_BLOCK_NORM_GAIN, s);
-    e = launch_pdl(block_norm_gain_kernel, dim3(a.H / 32), dim3(1024), 0, s, a, (const float *)scratch, grid);
+    e = launch_pdl(block_norm_gain_kernel, dim3(a.H / 16), dim3(1024), 0, s, a, (const float *)scratch, grid);
   }
   return e;
 }
