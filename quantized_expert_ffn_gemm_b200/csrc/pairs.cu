@@ -10,6 +10,11 @@
 // The sort is a stable counting sort: each block ranks a chunk of pairs (equal experts of a warp by
 // __match_any_sync, warps by a prefix over their counts), so the order is the same in every run.
 // Nothing here adds with atomics across blocks; sums run over j in order.
+//
+// The copies are bound by their bytes. 8192 tokens of ten bf16 rows of 2048: dispatch 60.7 us (369 MB, 56 us of
+// measured copy rate), collect 69 us (436 MB read and written, 61 us of which it reads rows in 4 KB pieces
+// scattered over 335 MB), its gradient 115 us (705 MB, 107 us). The sort before them is a chain of a few
+// dependent steps: about 9 us for 81,920 pairs in two launches, 4 us for 60 in one.
 #include <type_traits>
 
 #include "block.cuh"
