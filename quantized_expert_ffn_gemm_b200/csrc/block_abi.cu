@@ -23,6 +23,12 @@ moe_status width_status(int n) {
 
 bool pairs_ok(int T, int k) { return T >= 0 && k >= 1 && k <= kMaxK && (long long)T * k <= INT32_MAX; }
 
+// a gate for each mode but none; no tokens' gates may be no memory at all
+bool gate_ok(int mode, const float *gate, int T) {
+  if (mode == MOE_GATE_NONE) return !gate;
+  return (mode == MOE_GATE_CHANNEL || mode == MOE_GATE_TOKEN) && (gate || (mode == MOE_GATE_TOKEN && T == 0));
+}
+
 size_t sort_bytes(int T, int k, int E) { return kCtrlStride + sort_pairs_scratch((long long)T * k, E); }
 
 moe_status check_mx4(const moe_mx4_mat &m, int E, int N, int K) {
@@ -48,8 +54,7 @@ moe_status moe_block_norm(const void *r, int32_t r_type, const void *y, int32_t 
   if (st != MOE_OK) return st;
   if (T < 0 || !(eps >= 0.0f) || !type_ok(r_type) || (y && !type_ok(y_type)) || (u && !type_ok(u_type)))
     return MOE_ERR_INVALID_ARG;
-  if (gate_mode < MOE_GATE_NONE || gate_mode > MOE_GATE_TOKEN || (gate_mode != MOE_GATE_NONE) != (gate != nullptr))
-    return MOE_ERR_INVALID_ARG;
+  if (!gate_ok(gate_mode, gate, T)) return MOE_ERR_INVALID_ARG;
   if (!y && T > 0 && (post_gain || gate || rstd_y)) return MOE_ERR_INVALID_ARG;
   if ((rstd_y && !post_norm) || (!u && T > 0 && (pre_gain || rstd_u))) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
@@ -69,8 +74,7 @@ moe_status moe_block_norm_backward(const void *dr_out, const void *du, int32_t u
   const moe_status st = width_status(H);
   if (st != MOE_OK) return st;
   if (T < 0 || !type_ok(r_type) || (du && !type_ok(u_type)) || (y && !type_ok(y_type))) return MOE_ERR_INVALID_ARG;
-  if (gate_mode < MOE_GATE_NONE || gate_mode > MOE_GATE_TOKEN || (gate_mode != MOE_GATE_NONE) != (gate != nullptr))
-    return MOE_ERR_INVALID_ARG;
+  if (!gate_ok(gate_mode, gate, T)) return MOE_ERR_INVALID_ARG;
   if (d_gate && !gate) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(dr_out, du, r_out, rstd_u, y, rstd_y, post_gain, gate, pre_gain, dr, dy) ||
       !all_aligned(d_post_gain, d_gate, d_pre_gain))
@@ -155,7 +159,7 @@ moe_status moe_mx4_quantize(const void *x, int32_t type, int32_t T, int32_t K, c
                             const int32_t *kept, uint8_t *codes, uint8_t *scales, void *stream) {
   const moe_status st = width_status(K);
   if (st != MOE_OK) return st;
-  if (!type_ok(type) || !pairs_ok(T, row_of ? k : 1) || (kept && !row_of)) return MOE_ERR_INVALID_ARG;
+  if (!type_ok(type) || !pairs_ok(T, row_of ? k : 1) || (kept && !row_of && T > 0)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(x, row_of, codes, scales) || ((uintptr_t)kept & 3u)) return MOE_ERR_ALIGNMENT;

@@ -147,6 +147,7 @@ def test_backward_types(r, y, u, gate):
 def test_backward_longest_rows(y, u):
     """Rows of up to 256 KB: through shared memory where they fit, else read again from memory."""
     run_backward(dev(inputs(3, 16384, y=y, u=u)), 0.5)
+    run_backward(dev(inputs(5, 4160, BF16, y, u, "token")), 1.5)
 
 
 @pytest.mark.parametrize("H", [192, 4160])
