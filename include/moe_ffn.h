@@ -301,13 +301,16 @@ moe_status moe_router_topk_static(const uint16_t *x, int32_t T, int32_t H, const
  * nearest even. Results are the same in every run. The conventions above hold; shape rules: H, K
  * and N multiples of 64 up to 16384 (a multiple of 32 gives MOE_ERR_UNSUPPORTED, anything else
  * MOE_ERR_INVALID_ARG), 1 <= k <= min(E, 32), E <= 4096, T * k < 2^31. Outputs do not overlap inputs
- * unless said so. */
+ * unless said so. Router weights Wr that one of these calls writes (moe_mx4_dequantize apart) are safe for
+ * a router or layer call only after a synchronisation or a plainly launched kernel between the two:
+ * these kernels let their dependents start at their entry. */
 enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 };
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
 
 /* Bytes of device workspace that suffice for every block operator on T tokens with k slots, E
  * experts and rows of H values (0 for sizes they do not take). A workspace serves one stream at a
- * time; initialise it with moe_workspace_init. */
+ * time; initialise it with moe_workspace_init. One that is large enough for both may serve layer calls
+ * and block operators in turn. */
 size_t moe_block_workspace_bytes(int32_t T, int32_t k, int32_t E, int32_t H);
 
 /* The norms around a block:

@@ -29,7 +29,11 @@ bool gate_ok(int mode, const float *gate, int T) {
   return (mode == MOE_GATE_CHANNEL || mode == MOE_GATE_TOKEN) && (gate || (mode == MOE_GATE_TOKEN && T == 0));
 }
 
-size_t sort_bytes(int T, int k, int E) { return kCtrlStride + sort_pairs_scratch((long long)T * k, E); }
+// Scratch lies behind the whole control area: what the decode kernel keeps there from one launch to the next (its launch
+// counts, words tagged with them) stays valid, so a workspace may serve layers and these operators in turn.
+constexpr size_t kScratch = (kControlBytes + 255) / 256 * 256;
+size_t sort_bytes(int T, int k, int E) { return kScratch + sort_pairs_scratch((long long)T * k, E); }
+size_t norm_grad_bytes(int T, int H) { return kScratch + block_norm_grad_scratch(T, H); }
 
 moe_status check_mx4(const moe_mx4_mat &m, int E, int N, int K) {
   if (m.n_experts != E || m.rows != N || m.K != K || !m.codes || !m.scales) return MOE_ERR_INVALID_ARG;
@@ -42,7 +46,7 @@ extern "C" {
 
 size_t moe_block_workspace_bytes(int32_t T, int32_t k, int32_t E, int32_t H) {
   if (!pairs_ok(T, k) || E < 1 || E > kMaxE || k > E || width_status(H) != MOE_OK) return 0;
-  const size_t sort = sort_bytes(T, k, E), norm = kCtrlStride + block_norm_grad_scratch(T, H);
+  const size_t sort = sort_bytes(T, k, E), norm = norm_grad_bytes(T, H);
   return align_up(sort > norm ? sort : norm, 256);
 }
 
@@ -92,12 +96,12 @@ moe_status moe_block_norm_backward(const void *dr_out, const void *du, int32_t u
   if ((y != nullptr) != (dy != nullptr)) return MOE_ERR_INVALID_ARG;
   if (!y && (post_gain || gate || d_post_gain)) return MOE_ERR_INVALID_ARG;
   if (!du && (pre_gain || d_pre_gain)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kCtrlStride + block_norm_grad_scratch(T, H)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < norm_grad_bytes(T, H)) return MOE_ERR_WORKSPACE;
   if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
   const BlockNormGradArgs a{dr_out, du,     u_type,    r_out, y,        r_type,    y_type, T,  H,           post_norm ? 1 : 0,
                             rstd_u, rstd_y, post_gain, gate,  pre_gain, gate_mode, res_scale, dr, dy, d_post_gain,
                             d_gate, d_pre_gain};
-  float *scratch = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kCtrlStride);
+  float *scratch = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kScratch);
   return cuda_status(launch_block_norm_grad(a, scratch, s));
 }
 
@@ -116,7 +120,7 @@ moe_status moe_sort_pairs(const int32_t *idx, int32_t T, int32_t k, int32_t E, i
   if (!ws || ws_bytes < sort_bytes(T, k, E)) return MOE_ERR_WORKSPACE;
   if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
   return cuda_status(launch_sort_pairs(idx, T, k, E, counts, offsets, row_of, src,
-                                       reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kCtrlStride),
+                                       reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kScratch),
                                        static_cast<Ctrl *>(ws), s));
 }
 

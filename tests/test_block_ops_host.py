@@ -27,6 +27,13 @@ def test_workspace_bytes(lib):
         assert moe.block_workspace_bytes(*bad) == 0, bad
 
 
+def test_scratch_lies_behind_the_control_area(lib):
+    """What the decode kernel keeps in a workspace from call to call (624,896 bytes) is not scratch."""
+    assert moe.block_workspace_bytes(1, 1, 1, 64) > 624896
+    assert norm_grad(lib, wsb=1 << 19) == WORKSPACE
+    assert lib.moe_sort_pairs(P, 4, 2, 8, P, P, P, P, P, 1 << 19, None) == WORKSPACE
+
+
 def norm(lib, r=P, rt=0, y=P, yt=0, T=4, H=128, post=1, pg=P, gate=None, mode=0, eps=1e-6, prg=P, ro=P, u=P, ut=2, ry=P,
          ru=P):
     return lib.moe_block_norm(r, rt, y, yt, T, H, post, pg, gate, mode, 1.0, eps, prg, ro, u, ut, ry, ru, None)

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import quantized_expert_ffn_gemm_b200 as moe
+import synth
 from tests import block_ref as ref
+from tests.gpu_util import to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -208,3 +210,77 @@ def test_more_than_2_to_31_values():
     for s in (slice(0, 8), slice(139992, 140000)):
         _, few, _, rs = moe.block_norm(r[s].clone())
         assert torch.equal(u[s], few) and torch.equal(rstd[s], rs)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5])
+def test_one_workspace_for_layers_and_block_operators(T):
+    """The decode kernel keeps its launch counts and tagged words in the workspace from call to call; sorts and gradients
+    in between leave them alone, whatever they write."""
+    shape = synth.LayerShape("block_shared_ws", 8, 512, 32, 4, 256, synth.Q2, True, 1.1, seed=31)
+    x, Wr, b, routed, shared = to_dev(synth.make_layer(shape))
+    x = x[:T].contiguous()
+    run = lambda ws: moe.layer_forward(x, Wr, b, routed, shared, 4, ws)  # noqa: E731
+    want = run(moe.Workspace.for_layer(512, 32, 4, 256, True, T)).clone()
+    ws = moe.Workspace(max(moe.workspace_bytes(512, 32, 4, 256, True, 8), moe.block_workspace_bytes(3000, 4, 32, 2048)))
+    g = torch.Generator().manual_seed(T)
+    r, s = torch.randn(700, 2048, generator=g).cuda(), torch.rand(700, generator=g).cuda()
+    gain = torch.ones(2048, device="cuda")
+    for i in range(6):
+        n = 3000 if i % 2 else 7
+        idx = torch.rand(n, 32, generator=g).topk(4, 1).indices.to(torch.int32)
+        plan = moe.sort_pairs(idx.cuda(), 32, ws)
+        grad = moe.block_norm_backward(r, r, r, s, pre_gain=gain, ws=ws)
+        assert torch.equal(run(ws), want)
+        assert torch.equal(plan["row_of"].cpu(), ref.sort_pairs(idx, 32)["row_of"])
+        x64, d = r.double() * s.double()[:, None], r.double()
+        assert float((grad["d_pre_gain"].double() - (d * x64).sum(0)).abs().max()) <= 702 * 2.0 ** -24 * float(
+            (d * x64).abs().sum(0).max())
+    assert moe.read_device_error(ws) == 0
+    big = moe.block_workspace_bytes(3000, 4, 32, 2048)
+    assert big > moe.block_workspace_bytes(1, 1, 1, 64) > 0
+
+
+def test_rows_written_and_read_again_without_a_pause():
+    """A chain of small calls on the same buffers, each allowed to start while the one before ends: every reader sees what
+    its writer left, eagerly and in a replayed graph."""
+    T, k, H, n = 6, 10, 2048, 40
+    g = torch.Generator().manual_seed(11)
+    row_of = torch.randperm(T * k, generator=g).to(torch.int32).view(T, k).cuda()
+    xs = torch.randint(-8, 9, (n, T, H), generator=g).float().cuda()  # sums of k equal values are exact
+    rows = torch.zeros(T * k, H, device="cuda")
+    want = k * xs
+
+    def chain():
+        ys = []
+        for x in xs:
+            moe.dispatch(x, row_of, None, rows)
+            ys.append(moe.collect(rows, row_of))
+        return torch.stack(ys)
+
+    for _ in range(5):
+        assert torch.equal(chain(), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for sign in (-1, 1):
+        xs.mul_(-1)
+        rows.zero_()
+        graph.replay()
+        assert torch.equal(out, k * xs)
+
+
+def test_quantised_rows_and_products_without_a_pause():
+    """As above through the MXFP4 rows: quantised into the same memory (the allocator hands it out again) and multiplied."""
+    T, K, N, n = 3, 256, 64, 30
+    g = torch.Generator().manual_seed(12)
+    w = moe.mx4_quantize(torch.randint(-3, 4, (1, N, K), generator=g).float().cuda())
+    xs = torch.randint(-3, 4, (n, T, K), generator=g).float().cuda()  # MXFP4 holds these exactly
+    ws = moe.Workspace(256)
+    want = [moe.mx4_dequantize(moe.mx4_quantize(x), F32).double() @ moe.mx4_dequantize(w, F32)[0].double().T for x in xs]
+
+    def chain():
+        return torch.stack([moe.mx4_product(moe.mx4_quantize(x), w, dtype=F16, ws=ws) for x in xs])
+
+    for _ in range(5):
+        assert torch.equal(chain().double(), torch.stack(want))  # integers, far below 2^11: exact in fp16
+    assert moe.read_device_error(ws) == 0
