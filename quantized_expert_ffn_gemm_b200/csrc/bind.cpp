@@ -6,6 +6,7 @@
 // A tensor of another type, shape, layout or device than the call takes raises ValueError, a status of the
 // library raises the package's MoeError. The call runs on its tensors' device and that device's current stream.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -101,7 +102,24 @@ int32_t size32(int64_t n) {
   if (n > INT32_MAX) throw Refused("a size beyond 2^31 - 1");
   return (int32_t)n;
 }
-Tensor fresh(at::IntArrayRef sizes, const Tensor &like, ScalarType t) { return at::empty(sizes, like.options().dtype(t)); }
+Tensor fresh(at::IntArrayRef sizes, const Tensor &like, ScalarType t) {
+  return Tensor(at::detail::empty_cuda(sizes, t, like.device(), std::nullopt));
+}
+// Small outputs of one call in one allocation: tensors over parts of a buffer, each starting on 32 bytes.
+struct Parts {
+  const Tensor buf;
+  int64_t at = 0;
+  Parts(int64_t n, const Tensor &like, ScalarType t) : buf(fresh({n}, like, t)) {}
+  static int64_t round(int64_t n) { return (n + 7) / 8 * 8; }  // of four bytes each
+  Tensor take(at::IntArrayRef sizes) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(buf.storage()), buf.key_set(),
+                                                     buf.dtype());
+    impl->set_storage_offset(at);
+    impl->set_sizes_contiguous(sizes);
+    at += round(impl->numel());
+    return Tensor(std::move(impl));
+  }
+};
 void done(const char *fn, moe_status code) {
   if (code != MOE_OK) throw Status{fn, code};
 }
@@ -216,11 +234,13 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (r_out.scalar_type() != r.scalar_type()) throw Refused("r_out: another type than r");
     }
     Tensor u, rstd_y, rstd_u;
-    if (pre_norm) {
-      u = fresh({T, H}, r, ut);
-      rstd_u = fresh({T}, r, at::kFloat);
+    const bool close = y && post_norm;
+    if (pre_norm) u = fresh({T, H}, r, ut);
+    if (pre_norm || close) {
+      Parts parts((pre_norm + close) * Parts::round(T), r, at::kFloat);
+      if (pre_norm) rstd_u = parts.take({T});
+      if (close) rstd_y = parts.take({T});
     }
-    if (y && post_norm) rstd_y = fresh({T}, r, at::kFloat);
     done("moe_block_norm",
          moe_block_norm(r.data_ptr(), type_code(r.scalar_type()), ptr(y), y ? type_code(y->scalar_type()) : MOE_F32,
                         size32(T), size32(H), post_norm, ptr_as<float>(post), ptr_as<float>(gate), mode,
@@ -278,8 +298,9 @@ PyObject *sort_pairs(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const Space ws = workspace(c, a[2]);
     const int64_t T = idx.size(0), k = idx.size(1);
-    Tensor counts = fresh({E > 0 ? E : 1}, idx, at::kInt), offsets = fresh({(E > 0 ? E : 1) + 1}, idx, at::kInt);
-    Tensor row_of = fresh({T, k}, idx, at::kInt), src = fresh({T * k}, idx, at::kInt);
+    const int64_t ne = E > 0 ? E : 1;
+    Parts parts(Parts::round(ne) + Parts::round(ne + 1) + 2 * Parts::round(T * k), idx, at::kInt);
+    Tensor counts = parts.take({ne}), offsets = parts.take({ne + 1}), row_of = parts.take({T, k}), src = parts.take({T * k});
     done("moe_sort_pairs", moe_sort_pairs(idx.data_ptr<int32_t>(), size32(T), size32(k), (int32_t)E,
                                           counts.data_ptr<int32_t>(), offsets.data_ptr<int32_t>(),
                                           row_of.data_ptr<int32_t>(), src.data_ptr<int32_t>(), ws.p, ws.n, c.stream()));
