@@ -131,7 +131,8 @@ struct Space {
 };
 Space workspace(Call &c, PyObject *ws) {
   if (ws == Py_None) throw Refused("ws: this call needs a Workspace");
-  PyObject *buf = PyObject_GetAttrString(ws, "buf"), *n = buf ? PyObject_GetAttrString(ws, "nbytes") : nullptr;
+  static PyObject *const kBuf = PyUnicode_InternFromString("buf"), *const kBytes = PyUnicode_InternFromString("nbytes");
+  PyObject *buf = PyObject_GetAttr(ws, kBuf), *n = buf ? PyObject_GetAttr(ws, kBytes) : nullptr;
   if (!buf || !n) {
     Py_XDECREF(buf);
     PyErr_Clear();
@@ -270,9 +271,13 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Space ws = workspace(c, a[11]);
     Tensor dr = fresh({T, H}, r, r.scalar_type()), dy, d_post, d_gate, d_pre;
     if (y) dy = fresh({T, H}, r, y->scalar_type());
-    if (post) d_post = fresh({H}, r, at::kFloat);
-    if (gate) d_gate = fresh(gate->sizes(), r, at::kFloat);
-    if (pre) d_pre = fresh({H}, r, at::kFloat);
+    if (post || gate || pre) {
+      Parts parts(((post != nullptr) + (pre != nullptr)) * Parts::round(H) + (gate ? Parts::round(gate->numel()) : 0), r,
+                  at::kFloat);
+      if (post) d_post = parts.take({H});
+      if (gate) d_gate = parts.take(gate->sizes());
+      if (pre) d_pre = parts.take({H});
+    }
     auto p32 = [](const Tensor &t) { return t.defined() ? t.data_ptr<float>() : nullptr; };
     done("moe_block_norm_backward",
          moe_block_norm_backward(ptr(dr_out), ptr(du), du ? type_code(du->scalar_type()) : MOE_F32, r.data_ptr(),
