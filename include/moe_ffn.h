@@ -402,9 +402,10 @@ moe_status moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32
  *   out[r,n] = silu(A W_g^T)[r,n] * (A U_g^T)[r,n]       with up != NULL (gate and up projections)
  * a_codes / a_scales: n_rows rows; w (and up): n_experts = E experts of N = rows features; offsets
  * device int32 [E+1], offsets[0] = 0, monotone, offsets[E] <= n_rows (rows behind offsets[E] become
- * zero); NULL with E = 1: one group of all rows. out [n_rows,N] fp16 or bf16 (MOE_ERR_UNSUPPORTED for
- * fp32: the tensor cores' sums do not carry that precision). ws: its control area alone, for the error
- * word (MOE_ERR_TIMEOUT). */
+ * zero; offsets that are not so record MOE_ERR_DEVICE_CHECK, and out is then undefined); NULL with
+ * E = 1: one group of all rows. out [n_rows,N] fp16 or bf16 (MOE_ERR_UNSUPPORTED for fp32: the tensor
+ * cores' sums do not carry that precision). ws: its control area alone, for the error word (which also
+ * takes MOE_ERR_TIMEOUT). */
 moe_status moe_mx4_product(const uint8_t *a_codes, const uint8_t *a_scales, int32_t n_rows, const int32_t *offsets,
                            int32_t E, const moe_mx4_mat *w, const moe_mx4_mat *up, void *out, int32_t out_type,
                            void *ws, size_t ws_bytes, void *stream);

@@ -276,10 +276,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     if (UP) prefetch_map(&tm_u);
   }
   pdl_wait();
+  bool good;  // offsets that are no offsets: flagged, and no tile is worked on (groups could overlap without end)
   {  // tiles before each group: every thread sums a run of groups, then a block scan of the runs
     constexpr int kPer = (kMaxE + S::kThreads - 1) / S::kThreads;
     const int per = (args.E + S::kThreads - 1) / S::kThreads, g0 = tid * per;
-    int at[kPer + 1], mine = 0;  // a run's offsets, loaded in one round
+    int at[kPer + 1], mine = 0, bad = 0;  // a run's offsets, loaded in one round
 #pragma unroll
     for (int i = 0; i <= kPer; ++i)
       if (i <= per && g0 + i <= args.E) at[i] = args.offsets ? args.offsets[g0 + i] : i * args.n_rows;
@@ -288,7 +289,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       const int g = g0 + i;
       if (i >= per || g >= args.E) continue;
       const int s0 = min(max(at[i], 0), args.n_rows), s1 = min(max(at[i + 1], s0), args.n_rows);
-      if (s0 != at[i] || s1 != at[i + 1] || (g == 0 && s0 != 0)) set_device_error(ctrl, MOE_ERR_DEVICE_CHECK, g);
+      if (s0 != at[i] || s1 != at[i + 1] || (g == 0 && s0 != 0)) {
+        set_device_error(ctrl, MOE_ERR_DEVICE_CHECK, g);
+        bad = 1;
+      }
       at[i] = (s1 - s0 + NT - 1) / NT * args.m_tiles;
       mine += at[i];
     }
@@ -299,7 +303,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       if (lane >= o) incl += n;
     }
     if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
+    good = !__syncthreads_or(bad);
     int run = incl - mine;
     for (int w = 0; w < warp; ++w) run += s_warp[w];
 #pragma unroll
@@ -315,7 +319,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int total = s_pref[args.E], G = gridDim.x, nk = (args.K + kMxStageK - 1) / kMxStageK;
+  const int total = good ? s_pref[args.E] : 0, G = gridDim.x, nk = (args.K + kMxStageK - 1) / kMxStageK;
   const int n_my = total > (int)blockIdx.x ? (total - (int)blockIdx.x + G - 1) / G : 0;
 
   auto find_tile = [&](int tl) {

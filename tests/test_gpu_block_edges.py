@@ -284,3 +284,18 @@ def test_quantised_rows_and_products_without_a_pause():
     for _ in range(5):
         assert torch.equal(chain().double(), torch.stack(want))  # integers, far below 2^11: exact in fp16
     assert moe.read_device_error(ws) == 0
+
+
+def test_offsets_that_swing_are_work_for_nobody():
+    """Offsets 0, n, 0, n, ...: every second group would be all rows. The call flags them and multiplies nothing."""
+    n, E, K, N = 4000, 512, 256, 64
+    a = moe.mx4_quantize(torch.randn(n, K, generator=torch.Generator().manual_seed(5)).cuda())
+    w = moe.mx4_quantize(torch.randn(E, N, K, generator=torch.Generator().manual_seed(6)).cuda())
+    ws = moe.Workspace(256)
+    good = torch.linspace(0, n, E + 1).to(torch.int32).cuda()
+    want = moe.mx4_product(a, w, good, ws=ws)
+    swing = torch.tensor([0, n], dtype=torch.int32).repeat(E // 2 + 1)[:E + 1].cuda()
+    for up in (None, w):
+        moe.mx4_product(a, w, swing, up=up, ws=ws)
+        assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_CHECK
+    assert torch.equal(want, moe.mx4_product(a, w, good, ws=ws)) and moe.read_device_error(ws) == 0
