@@ -16,8 +16,9 @@
 //
 // Both are bound by the bytes of their rows, once a row's two dependent sums stop holding the memory up. 8192 rows of
 // 2048, fp32 stream, bf16 u: forward with fp32 y 36.6 us (235 MB, 35.8 us of measured copy rate); gradient with
-// bf16 y 54 us and 3 for the gains' sums (302 MB, 46 us): what it lacks is issue slots, 16 warps an SM with
-// 114 registers each. One row of one token is a launch and two reductions, 2.3 us in a graph.
+// bf16 y 54 us and 3 for the gains' sums (302 MB, 46 us): 28 rows a block behind one another, each with its two
+// sums, a ring to fill first and 5 MB of partial sums to write last (half the arithmetic instructions, by packed
+// pairs of fp32, left it at 54). One row of one token is a launch and two reductions, 2.3 us in a graph.
 #include <initializer_list>
 #include <type_traits>
 
