@@ -12,13 +12,14 @@
 //             d_pre_gain = sum_t du x;  d_post_gain = sum_t g gate v;  d_gate = sum g post_gain v
 // (sum over t for a gate a channel, over h for a gate a token). With A = sum_t g v (a token's gate
 // folded in), d_post_gain = gate A and d_gate = post_gain A for channel gates, so two sums a channel
-// are carried whatever the gate.
+// are carried whatever the gate. mean(q v) depends on mean(h x), but linearly: with e = dr' + rstd_u h,
+// c = rstd_u mean(h x) and f = gate * post_gain, g = e - c x and sum f g v = sum f v e - c sum f v x. So a row
+// takes one round of three sums, and each of them errs by no more than the terms of g do.
 //
 // Both are bound by the bytes of their rows, once a row's two dependent sums stop holding the memory up. 8192 rows of
 // 2048, fp32 stream, bf16 u: forward with fp32 y 36.6 us (235 MB, 35.8 us of measured copy rate); gradient with
-// bf16 y 54 us and 3 for the gains' sums (302 MB, 46 us): 28 rows a block behind one another, each with its two
-// sums, a ring to fill first and 5 MB of partial sums to write last (half the arithmetic instructions, by packed
-// pairs of fp32, left it at 54). One row of one token is a launch and two reductions, 2.3 us in a graph.
+// bf16 y 52.5 us and 3 for the gains' sums (302 MB, 46 us): a ring to fill first, 28 rows a block behind one another
+// and 5 MB of partial sums to write last. One row of one token is a launch and two reductions, 2.3 us in a graph.
 #include <initializer_list>
 #include <type_traits>
 
@@ -50,6 +51,32 @@ struct RowSum {
         if (o < nw) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     return v;
+  }
+};
+
+// Three such sums at once, with one barrier; the buffers alternate in the same way.
+struct RowSum3 {
+  float (*buf)[3][kNormWarps];
+  int tpr, k;
+  __device__ __forceinline__ void operator()(float v[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = warp_sum(v[i]);
+    if (tpr > 32) {
+      const int nw = tpr >> 5, lane = threadIdx.x & 31, w0 = (threadIdx.x >> 5) & ~(nw - 1);
+      float(*b)[kNormWarps] = buf[k];
+      k ^= 1;
+      if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) b[i][threadIdx.x >> 5] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) v[i] = b[i][w0 + (lane & (nw - 1))];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+        if (o < nw)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
   }
 };
 
@@ -167,44 +194,74 @@ __global__ void __launch_bounds__(KT, KT == 256 ? 3 : 1) block_norm_kernel(const
   }
 }
 
+// Two fp32 values in a register pair: one instruction computes on both, each rounded as by itself.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pack2(a, a); }
+__device__ __forceinline__ float2 unpack2(F2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 v) {
+  const float2 f = unpack2(v);
+  return f.x + f.y;
+}
+
 // Four values of a row, fp32 or 16-bit, as the gradient's rows pass through shared memory.
 template <bool F>
-__device__ __forceinline__ void get4(const uint8_t *plane, int i, bool bf16, float v[4]) {
+__device__ __forceinline__ void get4(const uint8_t *plane, int i, bool bf16, F2 v[2]) {
   if constexpr (F) {
-    const float4 x = reinterpret_cast<const float4 *>(plane)[i];
+    const ulonglong2 x = reinterpret_cast<const ulonglong2 *>(plane)[i];
     v[0] = x.x;
     v[1] = x.y;
-    v[2] = x.z;
-    v[3] = x.w;
   } else {
     const uint2 w = reinterpret_cast<const uint2 *>(plane)[i];
     const uint32_t p[2] = {w.x, w.y};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (bf16) {
-        v[2 * j] = __uint_as_float(p[j] << 16);
-        v[2 * j + 1] = __uint_as_float(p[j] & 0xffff0000u);
+        v[j] = pack2(__uint_as_float(p[j] << 16), __uint_as_float(p[j] & 0xffff0000u));
       } else {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
+        v[j] = pack2(f.x, f.y);
       }
     }
   }
 }
 template <bool F>
-__device__ __forceinline__ void put4(void *base, size_t i, bool bf16, const float v[4]) {
+__device__ __forceinline__ void put4(void *base, size_t i, bool bf16, const F2 v[2]) {
   if constexpr (F) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(base) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<ulonglong2 *>(static_cast<float *>(base) + i) = make_ulonglong2(v[0], v[1]);
   } else {
     uint32_t p[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+      const float2 f = unpack2(v[j]);
       if (bf16) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
         p[j] = *reinterpret_cast<const uint32_t *>(&b);
       } else {
-        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        const __half2 h = __floats2half2_rn(f.x, f.y);
         p[j] = *reinterpret_cast<const uint32_t *>(&h);
       }
     }
@@ -229,16 +286,16 @@ __device__ __forceinline__ void ring_wait(int newer) {  // all but the `newer` y
 constexpr int kRingStages = 4;
 
 // Rows of up to 8 tpr values, two groups of four a thread (values 4 lane .. and 4 tpr + 4 lane ..: accesses are whole
-// lines for every type). RF, YF, UF: r (and its gradients), y, u are fp32, else 16-bit. A row takes two
-// dependent sums, so the rows to come pass through a ring in shared memory meanwhile: each thread copies and
+// lines for every type). RF, YF, UF: r (and its gradients), y, u are fp32, else 16-bit. A row waits for its sums
+// (two rounds one behind the other took 54 us for 8192 rows of 2048, one round 52.5), so the rows to come pass through a ring in shared memory meanwhile: each thread copies and
 // reads its own values, no barrier needed. (The next row held in registers left room for 16 warps an SM
 // and took 69 us for 8192 rows of 2048.)
 template <int KT, bool RF, bool YF, bool UF>
 __global__ void __launch_bounds__(KT, KT == 256 ? kGradBlocks : 1)
 block_norm_grad_kernel(const BlockNormGradArgs a, float *__restrict__ part, int tpr, int stages) {
   extern __shared__ __align__(16) uint8_t s_ring[];
-  __shared__ float s_sum[2][kNormWarps];
-  RowSum row_sum{s_sum, tpr, 0};
+  __shared__ float s_sum[2][3][kNormWarps];
+  RowSum3 row_sums{s_sum, tpr, 0};
   constexpr int kR = KT * (RF ? 32 : 16), kU = KT * (UF ? 32 : 16), kY = KT * (YF ? 32 : 16);
   constexpr int kD0 = kR, kU0 = 2 * kR, kY0 = 2 * kR + kU, kBytes = 2 * kR + kU + kY;
   const int rows = KT / tpr, sub = threadIdx.x / tpr, lane = threadIdx.x & (tpr - 1);
@@ -247,14 +304,14 @@ block_norm_grad_kernel(const BlockNormGradArgs a, float *__restrict__ part, int 
   const int stride = gridDim.x * rows, first = blockIdx.x * rows + sub;
   const int at[2] = {4 * lane, 4 * tpr + 4 * lane};
   const bool in[2] = {at[0] < a.H, at[1] < a.H};
-  float sum_v[2][4], sum_x[2][4];  // sum over this thread's rows of g v (a token's gate folded in) and du x
-  float pre[2][4], f[2][4];        // pre_gain; post_gain times a channel's gate
+  F2 sum_v[2][2], sum_x[2][2];  // sum over this thread's rows of g v (a token's gate folded in) and du x
+  F2 pre[2][2], f[2][2];        // pre_gain; post_gain times a channel's gate
 #pragma unroll
   for (int g = 0; g < 2; ++g)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      sum_v[g][q] = sum_x[g][q] = 0.0f;
-      pre[g][q] = f[g][q] = 1.0f;
+    for (int q = 0; q < 2; ++q) {
+      sum_v[g][q] = sum_x[g][q] = both(0.0f);
+      pre[g][q] = f[g][q] = both(1.0f);
     }
   pdl_launch_dependents();
   pdl_wait();
@@ -280,13 +337,13 @@ block_norm_grad_kernel(const BlockNormGradArgs a, float *__restrict__ part, int 
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     if (!in[g]) continue;
-    float w[4];
+    F2 w[2];
     if (a.pre_gain) get4<true>(reinterpret_cast<const uint8_t *>(a.pre_gain), at[g] / 4, false, pre[g]);
     if (a.post_gain) get4<true>(reinterpret_cast<const uint8_t *>(a.post_gain), at[g] / 4, false, f[g]);
     if (a.gate_mode == MOE_GATE_CHANNEL) {
       get4<true>(reinterpret_cast<const uint8_t *>(a.gate), at[g] / 4, false, w);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) f[g][q] *= w[q];
+      for (int q = 0; q < 2; ++q) f[g][q] = mul2(f[g][q], w[q]);
     }
   }
   float su_n = 0.0f, sy_n = 1.0f, tok_n = 1.0f;  // the next row's statistics and gate
@@ -306,79 +363,77 @@ block_norm_grad_kernel(const BlockNormGradArgs a, float *__restrict__ part, int 
     fetch(t + (long long)(stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
     ring_wait(stages - 1);
     const uint8_t *m = s_ring + stage * kBytes;
-    float x[2][4], h[2][4], m_u = 0.0f;
-    if (a.du) {
+    F2 x[2][2], e[2][2], v[2][2], dot[3] = {both(0.0f), both(0.0f), both(0.0f)};
+    const F2 su2 = both(su), sy2 = both(sy), tok2 = both(tok), res2 = both(a.res_scale);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (!(live && in[g])) continue;
-        const int slot = g * KT + threadIdx.x;
-        get4<RF>(m, slot, rb, x[g]);
-        get4<UF>(m + kU0, slot, ub, h[g]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          x[g][q] *= su;
-          const float ux = h[g][q] * x[g][q];
-          sum_x[g][q] += ux;
-          m_u = fmaf(pre[g][q], ux, m_u);
-          h[g][q] *= pre[g][q];
-        }
-      }
-      m_u = row_sum(m_u) * inv_h;
-    }
-    float m_y = 0.0f;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {  // h becomes g, then gate post_gain g; x becomes v
+    for (int g = 0; g < 2; ++g) {
       if (!(live && in[g])) continue;
       const int slot = g * KT + threadIdx.x;
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (a.dr_out) get4<RF>(m + kD0, slot, rb, d);
+      e[g][0] = e[g][1] = both(0.0f);
+      if (a.dr_out) get4<RF>(m + kD0, slot, rb, e[g]);
+      if (a.du) {
+        F2 h[2];
+        get4<RF>(m, slot, rb, x[g]);
+        get4<UF>(m + kU0, slot, ub, h);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        h[g][q] = a.du ? fmaf(su, fmaf(-x[g][q], m_u, h[g][q]), d[q]) : d[q];
-        d[q] = a.res_scale * h[g][q];
+        for (int q = 0; q < 2; ++q) {
+          x[g][q] = mul2(x[g][q], su2);
+          sum_x[g][q] = fma2(h[q], x[g][q], sum_x[g][q]);
+          h[q] = mul2(h[q], pre[g][q]);
+          dot[0] = fma2(h[q], x[g][q], dot[0]);
+          e[g][q] = fma2(su2, h[q], e[g][q]);
+        }
       }
-      put4<RF>(a.dr, base + at[g], rb, d);
       if (a.y) {
-        get4<YF>(m + kY0, slot, yb, x[g]);
+        get4<YF>(m + kY0, slot, yb, v[g]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          x[g][q] *= sy;
-          const float hv = h[g][q] * x[g][q];
-          sum_v[g][q] = fmaf(tok, hv, sum_v[g][q]);
-          m_y = fmaf(f[g][q], hv, m_y);
-          h[g][q] *= f[g][q];
+        for (int q = 0; q < 2; ++q) {
+          v[g][q] = mul2(v[g][q], sy2);
+          const F2 fv = mul2(f[g][q], v[g][q]);
+          dot[1] = fma2(fv, e[g][q], dot[1]);
+          if (a.du) dot[2] = fma2(fv, x[g][q], dot[2]);
         }
       }
     }
-    if (a.y) {
-      const bool token_grad = a.d_gate && a.gate_mode == MOE_GATE_TOKEN;
-      if (a.post_norm || token_grad) m_y = row_sum(m_y);
-      if (token_grad && live && lane == 0) a.d_gate[t] = m_y;
-      const float mean = a.post_norm ? m_y * inv_h : 0.0f, scale = sy * tok;
+    float sums[3] = {sum2(dot[0]), sum2(dot[1]), sum2(dot[2])};
+    row_sums(sums);
+    const float c = su * (sums[0] * inv_h), m_y = fmaf(-c, sums[2], sums[1]);
+    if (a.d_gate && a.gate_mode == MOE_GATE_TOKEN && live && lane == 0) a.d_gate[t] = m_y;
+    const F2 neg_c = both(-c), neg_mean = both(a.post_norm ? -m_y * inv_h : 0.0f), scale = both(sy * tok);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (!(live && in[g])) continue;
+    for (int g = 0; g < 2; ++g) {  // e becomes g
+      if (!(live && in[g])) continue;
+      F2 o[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[g][q] = scale * fmaf(-x[g][q], mean, h[g][q]);
-        put4<YF>(a.dy, base + at[g], yb, h[g]);
+      for (int q = 0; q < 2; ++q) {
+        if (a.du) e[g][q] = fma2(x[g][q], neg_c, e[g][q]);
+        o[q] = mul2(res2, e[g][q]);
       }
+      put4<RF>(a.dr, base + at[g], rb, o);
+      if (!a.y) continue;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        sum_v[g][q] = fma2(tok2, mul2(e[g][q], v[g][q]), sum_v[g][q]);
+        o[q] = mul2(scale, fma2(v[g][q], neg_mean, mul2(f[g][q], e[g][q])));
+      }
+      put4<YF>(a.dy, base + at[g], yb, o);
     }
     stage = stage + 1 == stages ? 0 : stage + 1;
   }
   if (!part) return;
   // this block's sums: the row groups joined in shared memory in order, then one row of partials
   if (rows > 1) {
-    __shared__ float s_p[2][128 * 8];
+    __shared__ __align__(16) float s_p[2][128 * 8];
     for (int r = 0; r < rows; ++r) {
       __syncthreads();
       if (sub != r) continue;
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float *pv = &s_p[0][at[g] + q], *px = &s_p[1][at[g] + q];
-          *pv = sum_v[g][q] += r ? *pv : 0.0f;
-          *px = sum_x[g][q] += r ? *px : 0.0f;
+        for (int q = 0; q < 2; ++q) {
+          F2 *pv = reinterpret_cast<F2 *>(&s_p[0][at[g] + 2 * q]), *px = reinterpret_cast<F2 *>(&s_p[1][at[g] + 2 * q]);
+          *pv = sum_v[g][q] = r ? add2(sum_v[g][q], *pv) : sum_v[g][q];
+          *px = sum_x[g][q] = r ? add2(sum_x[g][q], *px) : sum_x[g][q];
         }
     }
     if (sub != rows - 1) return;
