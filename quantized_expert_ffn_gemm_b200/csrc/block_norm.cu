@@ -18,7 +18,7 @@
 //
 // Both are bound by the bytes of their rows, once a row's two dependent sums stop holding the memory up. 8192 rows of
 // 2048, fp32 stream, bf16 u: forward with fp32 y 36.6 us (235 MB, 35.8 us of measured copy rate); gradient with
-// bf16 y 52.5 us and 3 for the gains' sums (302 MB, 46 us): a ring to fill first, 28 rows a block behind one another
+// bf16 y 50.9 us and 3 for the gains' sums (302 MB, 46 us): a ring to fill first, 28 rows a block behind one another
 // and 5 MB of partial sums to write last. One row of one token is a launch and two reductions, 2.3 us in a graph.
 #include <initializer_list>
 #include <type_traits>
@@ -287,7 +287,7 @@ constexpr int kRingStages = 4;
 
 // Rows of up to 8 tpr values, two groups of four a thread (values 4 lane .. and 4 tpr + 4 lane ..: accesses are whole
 // lines for every type). RF, YF, UF: r (and its gradients), y, u are fp32, else 16-bit. A row waits for its sums
-// (two rounds one behind the other took 54 us for 8192 rows of 2048, one round 52.5), so the rows to come pass through a ring in shared memory meanwhile: each thread copies and
+// (two rounds one behind the other took 54.2 us for 8192 rows of 2048, one round 50.9), so the rows to come pass through a ring in shared memory meanwhile: each thread copies and
 // reads its own values, no barrier needed. (The next row held in registers left room for 16 warps an SM
 // and took 69 us for 8192 rows of 2048.)
 template <int KT, bool RF, bool YF, bool UF>
