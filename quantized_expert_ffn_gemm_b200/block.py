@@ -4,8 +4,9 @@ expert and collected again (each with its gradient), MXFP4 rows and their produc
 Only arguments are marshalled on the way to the library, in the compiled module _bind (csrc/bind.cpp): these
 operators are called with a microsecond or two of work for the GPU, and ctypes alone took longer. Tensors are
 contiguous CUDA tensors of one device; a call runs on that device's current stream, whichever device is
-current, and allocates its outputs unless they are given (a call's small ones as parts of one allocation). A tensor of another type, shape, layout or device
-than the call takes raises ValueError; what the library refuses raises MoeError.
+current, and allocates its outputs unless they are given (a call's small ones as parts of one allocation). A
+tensor of another type, shape, layout or device than the call takes raises ValueError; what the library refuses
+raises MoeError.
 """
 from __future__ import annotations
 
