@@ -583,9 +583,10 @@ __global__ void __launch_bounds__(512, 1) block_norm_grad_long_kernel(const Bloc
   for (int c = 0; c < CH; ++c) {
     const int i = lane + c * tpr;
     if (i >= H8) continue;
+    // 16 bytes a store: the scratch is aligned as the workspace is, which may start on any 16 bytes
     float *p = part + (size_t)blockIdx.x * 2 * a.H + 8 * i;
-    store8(p, kF32Wide, 0, sum_v[c]);
-    store8(p + a.H, kF32Wide, 0, sum_x[c]);
+    store8(p, MOE_F32, 0, sum_v[c]);
+    store8(p + a.H, MOE_F32, 0, sum_x[c]);
   }
 }
 

@@ -1,5 +1,7 @@
 """The block operators on calls that are allowed and unusual: tensors that start on 16 bytes but not on 32, outputs left
 out at the C interface, no rows at all, tensors of more than 2^31 values, and workspaces that are too small."""
+import types
+
 import pytest
 import torch
 
@@ -299,3 +301,30 @@ def test_offsets_that_swing_are_work_for_nobody():
         moe.mx4_product(a, w, swing, up=up, ws=ws)
         assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_CHECK
     assert torch.equal(want, moe.mx4_product(a, w, good, ws=ws)) and moe.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("T,H", [(7, 192), (300, 2048), (7, 4160), (3, 16384)])
+def test_workspace_on_16_bytes(T, H):
+    """Scratch behind a workspace that starts 16 bytes behind a 256-byte boundary: the same results as on the boundary."""
+    g = torch.Generator().manual_seed(H)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    r, y, dr, du, gain, gate = n(T, H), n(T, H), n(T, H), n(T, H), n(H), n(H)
+    ry, ru = (v.square().mean(1).rsqrt() for v in (y, r))
+    need = moe.block_workspace_bytes(T, H=H)
+    idx = torch.randint(-1, 32, (5000, 2), generator=g, dtype=torch.int32).cuda()
+
+    def results(at, nbytes):
+        buf = shifted(torch.zeros(nbytes, dtype=torch.uint8), at) if at else torch.zeros(nbytes, dtype=torch.uint8,
+                                                                                         device="cuda")
+        ws = types.SimpleNamespace(buf=buf, nbytes=nbytes)
+        grad = moe.block_norm_backward(dr, du, r, ru, y, ry, post_gain=gain, gate=gate, pre_gain=gain, ws=ws)
+        return list(grad.values())
+
+    def sorts(at):
+        nbytes = moe.block_workspace_bytes(5000, 2, 32)
+        buf = shifted(torch.zeros(nbytes, dtype=torch.uint8), at) if at else torch.zeros(nbytes, dtype=torch.uint8,
+                                                                                         device="cuda")
+        return list(moe.sort_pairs(idx, 32, types.SimpleNamespace(buf=buf, nbytes=nbytes)).values())
+
+    assert all(torch.equal(a, b) for a, b in zip(results(0, need), results(16, need)))
+    assert all(torch.equal(a, b) for a, b in zip(sorts(0), sorts(16)))
