@@ -303,9 +303,10 @@ PyObject *sort_pairs(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const Space ws = workspace(c, a[2]);
     const int64_t T = idx.size(0), k = idx.size(1);
-    const int64_t ne = E > 0 ? E : 1;
-    Parts parts(Parts::round(ne) + Parts::round(ne + 1) + 2 * Parts::round(T * k), idx, at::kInt);
-    Tensor counts = parts.take({ne}), offsets = parts.take({ne + 1}), row_of = parts.take({T, k}), src = parts.take({T * k});
+    // what the library will refuse takes no memory: E alone, no tensor's size, says how much that would be
+    if (!moe_block_workspace_bytes(size32(T), size32(k), (int32_t)E, 64)) throw Status{"moe_sort_pairs", MOE_ERR_INVALID_ARG};
+    Parts parts(Parts::round(E) + Parts::round(E + 1) + 2 * Parts::round(T * k), idx, at::kInt);
+    Tensor counts = parts.take({E}), offsets = parts.take({E + 1}), row_of = parts.take({T, k}), src = parts.take({T * k});
     done("moe_sort_pairs", moe_sort_pairs(idx.data_ptr<int32_t>(), size32(T), size32(k), (int32_t)E,
                                           counts.data_ptr<int32_t>(), offsets.data_ptr<int32_t>(),
                                           row_of.data_ptr<int32_t>(), src.data_ptr<int32_t>(), ws.p, ws.n, c.stream()));
