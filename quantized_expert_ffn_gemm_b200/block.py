@@ -102,8 +102,9 @@ def block_norm_backward(dr_out: Optional[torch.Tensor], du: Optional[torch.Tenso
                         pre_gain: Optional[torch.Tensor] = None, post_norm: bool = True, ws=None) -> dict:
     """Gradients of block_norm: a dict of dr, dy, d_post_gain, d_gate and d_pre_gain.
 
-    dr_out and du reach r' and u (None: nothing does); r_out, rstd_u, y and rstd_y as the forward call
-    took and returned them. An entry is None where block_norm had no such argument."""
+    dr_out and du reach r' and u (None: nothing does; not both); r_out, rstd_u, y and rstd_y as the forward call
+    took and returned them (rstd_u is not read without du). An entry is None where block_norm had no such
+    argument; without du d_pre_gain is zero."""
     dr, dy, d_post, d_gate, d_pre = (_b or _load()).block_norm_backward(
         dr_out, du, r_out, rstd_u, y, rstd_y, post_gain, gate, res_scale, pre_gain, post_norm, ws)
     return {"dr": dr, "dy": dy, "d_post_gain": d_post, "d_gate": d_gate, "d_pre_gain": d_pre}

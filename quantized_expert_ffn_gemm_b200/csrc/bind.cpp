@@ -284,8 +284,9 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                  type_code(r.scalar_type()), ptr_as<float>(rstd_u), ptr(y),
                                  y ? type_code(y->scalar_type()) : MOE_F32, ptr_as<float>(rstd_y), size32(T), size32(H),
                                  post_norm, ptr_as<float>(post), ptr_as<float>(gate), mode, number("res_scale", a[8]),
-                                 ptr_as<float>(pre), dr.data_ptr(), y ? dy.data_ptr() : nullptr, p32(d_post), p32(d_gate),
-                                 p32(d_pre), ws.p, ws.n, c.stream()));
+                                 du ? ptr_as<float>(pre) : nullptr, dr.data_ptr(), y ? dy.data_ptr() : nullptr, p32(d_post),
+                                 p32(d_gate), du ? p32(d_pre) : nullptr, ws.p, ws.n, c.stream()));
+    if (pre && !du) d_pre.zero_();  // nothing reaches u: the library takes pre_gain with du alone
     return tuple_of(dr, dy, d_post, d_gate, d_pre);
   });
 }

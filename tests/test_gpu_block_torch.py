@@ -24,3 +24,21 @@ def test_numbers_of_experts_out_of_range_take_no_memory():
     for E in (-1, 1 << 31):
         with pytest.raises(ValueError, match="E"):
             moe.sort_pairs(idx, E, ws)
+
+
+@pytest.mark.parametrize("H", [128, 4160])
+def test_backward_of_a_gain_that_no_gradient_reaches(H):
+    """du None: nothing reaches u. pre_gain's gradient is zero, the others are those of a call without pre_gain."""
+    T = 5
+    g = torch.Generator().manual_seed(H)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    r, y, dr, gain, gate = n(T, H), n(T, H), n(T, H), n(H), n(H)
+    ry = y.square().mean(1).rsqrt()
+    ws = moe.Workspace(moe.block_workspace_bytes(T, H=H))
+    args = dict(post_gain=gain, gate=gate, ws=ws)
+    want = moe.block_norm_backward(dr, None, r, None, y, ry, **args)
+    got = moe.block_norm_backward(dr, None, r, None, y, ry, pre_gain=gain, **args)
+    assert want["d_pre_gain"] is None and got["d_pre_gain"].shape == (H,) and bool((got["d_pre_gain"] == 0).all())
+    assert all(torch.equal(got[m], want[m]) for m in ("dr", "dy", "d_post_gain", "d_gate"))
+    none = moe.block_norm_backward(dr[:0], None, r[:0], None, y[:0], ry[:0], pre_gain=gain, **args)
+    assert bool((none["d_pre_gain"] == 0).all())
