@@ -78,6 +78,8 @@ def bind(lib):
 def block_workspace_bytes(T: int, k: int = 1, E: int = 1, H: int = 64) -> int:
     """Bytes of a Workspace that suffices for every block operator of these sizes (0: sizes not taken)."""
     import quantized_expert_ffn_gemm_b200 as moe
+    if not all(0 <= n < 1 << 31 for n in (T, k, E, H)):  # ctypes would cut them to 32 bits
+        return 0
     return int(moe.lib().moe_block_workspace_bytes(T, k, E, H))
 
 

@@ -638,8 +638,9 @@ int threads_of(int H) { return tpr_of(H) <= 256 ? 256 : 512; }
 
 int blocks_of(int T, int H, int per_sm) {  // per_sm: blocks of 256 threads an SM holds
   const int threads = threads_of(H), rows = threads / tpr_of(H);
-  const int want = (T + rows - 1) / rows, cap = num_sms() * (per_sm * 256 / threads);
-  return want < cap ? want : cap;
+  const int cap = num_sms() * (per_sm * 256 / threads);
+  const long long want = ((long long)T + rows - 1) / rows;
+  return want < cap ? (int)want : cap;
 }
 int norm_blocks(int T, int H) { return blocks_of(T, H, threads_of(H) == 256 ? 3 : 2); }
 int grad_blocks(int T, int H) { return blocks_of(T, H, threads_of(H) == 256 ? kGradBlocks : 2); }
@@ -672,9 +673,10 @@ template <int KT, bool RF, bool YF, bool UF>
 cudaError_t run_grad(const BlockNormGradArgs &a, float *part, int grid, cudaStream_t s) {
   constexpr int kBytes = KT * (2 * (RF ? 32 : 16) + (YF ? 32 : 16) + (UF ? 32 : 16));
   constexpr int kFit = 208 * 1024 / (KT == 256 ? kGradBlocks : 1) / kBytes;
-  const int tpr = tpr_of(a.H), rows = (a.T + KT / tpr - 1) / (KT / tpr);
+  const int tpr = tpr_of(a.H), side = KT / tpr;
+  const long long rows = ((long long)a.T + side - 1) / side, each = (rows + grid - 1) / grid;
   int stages = kFit < kRingStages ? kFit : kRingStages;
-  if (stages > (rows + grid - 1) / grid) stages = (rows + grid - 1) / grid;  // no more than a block's rows
+  if (stages > each) stages = (int)each;  // no more than a block's rows
   static_assert(kFit >= 1, "a row fits");
   const cudaError_t e = smem_limit_once(block_norm_grad_kernel<KT, RF, YF, UF>, kRingStages * kBytes < 208 * 1024
                                                                                    ? kRingStages * kBytes

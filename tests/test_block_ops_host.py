@@ -147,3 +147,14 @@ def test_tensors_of_another_kind_are_refused():
     for call, word in calls:
         with pytest.raises(ValueError, match=word):
             call()
+
+
+def test_workspace_bytes_at_the_ends_of_the_sizes(lib):
+    """As many tokens as an int32 holds, and sizes that it does not hold, which are not cut to 32 bits."""
+    most = (1 << 31) - 1
+    for H in (64, 1088, 2048, 4096, 8256, 16384):
+        few, near, last = (moe.block_workspace_bytes(T, 1, 1, H) for T in (most // 2, most - 64, most))
+        assert few <= near <= last < 1 << 28, H  # 2 M chunks' counts or 296 blocks' sums
+    for T, k, E, H in ((1 << 32) + 1, 1, 1, 64), (1, 1, 1, (1 << 32) + 64), (1, (1 << 32) + 1, 4, 64), (1 << 31, 1, 1, 64), (
+            -(1 << 32) + 1, 1, 1, 64):
+        assert moe.block_workspace_bytes(T, k, E, H) == 0, (T, k, E, H)
