@@ -298,12 +298,13 @@ moe_status moe_router_topk_static(const uint16_t *x, int32_t T, int32_t H, const
  * its gradient, and MXFP4 rows with their product per expert. Values are fp32, fp16 or bf16 (a
  * MOE_F32 / MOE_F16 / MOE_BF16 argument names the type of the tensor before it); gains, gates,
  * routing weights and statistics are fp32, sums are carried in fp32 and a result is rounded once, to
- * nearest even. Results are the same in every run. The conventions above hold; shape rules: H, K
- * and N multiples of 64 up to 16384 (a multiple of 32 gives MOE_ERR_UNSUPPORTED, anything else
- * MOE_ERR_INVALID_ARG), 1 <= k <= min(E, 32), E <= 4096, T * k < 2^31. Outputs do not overlap inputs
- * unless said so. Router weights Wr that one of these calls writes (moe_mx4_dequantize apart) are safe for
- * a router or layer call only after a synchronisation or a plainly launched kernel between the two:
- * these kernels let their dependents start at their entry. */
+ * nearest even (beyond fp16's range to +-inf; of these calls moe_mx4_product alone records that).
+ * Results are the same in every run. The conventions above hold; shape rules: H, K and N multiples
+ * of 64 up to 16384 (a multiple of 32 gives MOE_ERR_UNSUPPORTED, anything else MOE_ERR_INVALID_ARG),
+ * 1 <= k <= min(E, 32), E <= 4096, T * k < 2^31. Outputs do not overlap inputs unless said so. Router
+ * weights Wr that one of these calls writes (moe_mx4_dequantize apart) are safe for a router or layer
+ * call only after a synchronisation or a plainly launched kernel between the two: these kernels let
+ * their dependents start at their entry. */
 enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 };
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
 
@@ -404,8 +405,8 @@ moe_status moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32
  * device int32 [E+1], offsets[0] = 0, monotone, offsets[E] <= n_rows (rows behind offsets[E] become
  * zero; offsets that are not so record MOE_ERR_DEVICE_CHECK, and out is then undefined); NULL with
  * E = 1: one group of all rows. out [n_rows,N] fp16 or bf16 (MOE_ERR_UNSUPPORTED for fp32: the tensor
- * cores' sums do not carry that precision). ws: its control area alone, for the error word (which also
- * takes MOE_ERR_TIMEOUT). */
+ * cores' sums do not carry that precision). A result that does not fit fp16 becomes +-inf and records
+ * MOE_ERR_RANGE. ws: its control area alone, for the error word (which also takes MOE_ERR_TIMEOUT). */
 moe_status moe_mx4_product(const uint8_t *a_codes, const uint8_t *a_scales, int32_t n_rows, const int32_t *offsets,
                            int32_t E, const moe_mx4_mat *w, const moe_mx4_mat *up, void *out, int32_t out_type,
                            void *ws, size_t ws_bytes, void *stream);

@@ -124,19 +124,24 @@ __device__ __forceinline__ uint16_t cvt16(float v) {
   else return __half_as_ushort(__float2half_rn(v));
 }
 // n of a lane's values of C consecutive rows to those rows, N values apart. The type is known at compile time and a
-// whole chunk is stored without tests: with both decided value by value a store took 70 cycles.
+// whole chunk is stored without tests: with both decided value by value a store took 70 cycles. `top` becomes the largest
+// magnitude stored as fp16 (one instruction a value), so that what rounds to an infinity is seen once a launch.
 template <bool BF, int C>
-__device__ __forceinline__ void store_rows(uint16_t *o, int N, const float y[C], int n) {
+__device__ __forceinline__ void store_rows(uint16_t *o, int N, const float y[C], int n, float &top) {
   if (n >= C) {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       *o = cvt16<BF>(y[j]);
+      if constexpr (!BF) top = fmaxf(top, fabsf(y[j]));
       o += N;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      if (j < n) *o = cvt16<BF>(y[j]);
+      if (j < n) {
+        *o = cvt16<BF>(y[j]);
+        if constexpr (!BF) top = fmaxf(top, fabsf(y[j]));
+      }
       o += N;
     }
   }
@@ -454,6 +459,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int pair = (q & 1) + 2 * who;
     float *swap = reinterpret_cast<float *>(gbase + S::kSwap) + pair * 4 * 256;
     int turn = 0;
+    float top = 0.0f;
     bool ok = true;  // after a time-out a warp goes on through its partner's barriers, without waiting again
     for (int tl = who; tl < n_my; tl += 2) {
       const MxTile t = tile_at(tl);
@@ -485,12 +491,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
               const float gate = up_warp ? other : own, upv = up_warp ? own : other;
               y[j] = __fdividef(gate, 1.0f + __expf(-gate)) * upv;
             }
-            store_rows<BF, 8>(up_warp ? o + 8 * (size_t)args.N : o, args.N, y, up_warp ? left - 8 : left);
+            store_rows<BF, 8>(up_warp ? o + 8 * (size_t)args.N : o, args.N, y, up_warp ? left - 8 : left, top);
           } else {
             float y[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(x[j]);
-            store_rows<BF, 16>(o, args.N, y, left);
+            store_rows<BF, 16>(o, args.N, y, left, top);
           }
         };
         mx_ld16(acc, v[0]);
@@ -509,6 +515,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty(b));
+    }
+    // 65520 is the first magnitude that rounds to an fp16 infinity; a NaN is not larger than anything
+    if constexpr (!BF) {
+      if (__any_sync(0xffffffffu, top >= 65520.0f) && lane == 0) set_device_error(ctrl, MOE_ERR_RANGE, 47);
     }
     // rows behind the last group
     const int kept = args.offsets ? mx_group(args, args.E - 1).y : args.n_rows;

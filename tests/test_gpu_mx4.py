@@ -194,3 +194,42 @@ def test_product_flags_offsets_that_are_no_offsets():
         moe.mx4_product(a, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), ws=ws)
         assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_CHECK, bad
     assert torch.equal(good, moe.mx4_product(a, w, offsets.cuda(), ws=ws)) and moe.read_device_error(ws) == 0
+
+
+def block_values(*values):
+    """A row of 32 values a block, all but the first zero."""
+    x = torch.zeros(1, 32 * len(values))
+    x[0, ::32] = torch.tensor(values)
+    return x
+
+
+@pytest.mark.parametrize("rows", [1, 40, 200])
+def test_product_flags_results_beyond_fp16(rows):
+    """A sum that rounds to an fp16 infinity is recorded, the largest that rounds to 65504 is not; bf16 holds both."""
+    ws = moe.Workspace(256)
+    one = moe.mx4_quantize(block_values(1.0, 1.0, 1.0, 1.0).expand(64, -1).contiguous()[None].cuda())
+    for parts, flagged in (((65536.0, -32.0, 0, 0), False), ((65536.0, -16.0, -1.0, 0), False),
+                           ((65536.0, -16.0, 0, 0), True), ((-65536.0, 0, 0, 0), True), ((98304.0, 0, 0, 0), True)):
+        x = torch.zeros(rows, 128)
+        x[rows // 2] = block_values(*parts)
+        a = moe.mx4_quantize(x.cuda())
+        for dtype, bad in ((F16, flagged), (BF16, False)):
+            out = moe.mx4_product(a, one, dtype=dtype, ws=ws)
+            assert torch.equal(out[rows // 2].cpu(), torch.full((64,), sum(parts)).to(dtype))
+            assert moe.read_device_error(ws) == (moe.MOE_ERR_RANGE if bad else moe.MOE_OK), (parts, dtype)
+    # gate and up: 512 * 512
+    a = moe.mx4_quantize(block_values(512.0, 0).expand(rows, -1).contiguous().cuda())
+    w = moe.mx4_quantize(block_values(1.0, 0).expand(64, -1).contiguous()[None].cuda())
+    for dtype, bad in ((F16, moe.MOE_ERR_RANGE), (BF16, moe.MOE_OK)):
+        moe.mx4_product(a, w, up=w, dtype=dtype, ws=ws)
+        assert moe.read_device_error(ws) == bad
+
+
+def test_product_flags_nothing_but_results():
+    """Rows of other groups beside a tile's own are multiplied with it and no result: they are not flagged. Nor is NaN."""
+    ws = moe.Workspace(256)
+    a = moe.mx4_quantize(torch.cat([block_values(1.0, 0), block_values(32768.0, 0), block_values(float("nan"), 0)]).cuda())
+    w = moe.mx4_quantize(torch.stack([block_values(32768.0, 0).expand(64, -1), block_values(1.0, 0).expand(64, -1)]).cuda())
+    off = torch.tensor([0, 1, 3], dtype=torch.int32).cuda()
+    out = moe.mx4_product(a, w, off, ws=ws)
+    assert bool((out[:2] == 32768).all()) and bool(out[2].isnan().all()) and moe.read_device_error(ws) == moe.MOE_OK
