@@ -1,10 +1,13 @@
 """MXFP4 rows and their product per expert against fp64 (tests/block_ref.py, which states the bounds).
 
 Codes and scale bytes are equal bit for bit; reading back is exact."""
+import ctypes
+
 import pytest
 import torch
 
 import quantized_expert_ffn_gemm_b200 as moe
+from quantized_expert_ffn_gemm_b200.block import Mx4Mat
 from tests import block_ref as ref
 from tests.block_ref import close, rounded
 
@@ -233,3 +236,24 @@ def test_product_flags_nothing_but_results():
     off = torch.tensor([0, 1, 3], dtype=torch.int32).cuda()
     out = moe.mx4_product(a, w, off, ws=ws)
     assert bool((out[:2] == 32768).all()) and bool(out[2].isnan().all()) and moe.read_device_error(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("up", [False, True])
+def test_product_with_bad_offsets_stays_in_its_rows(up):
+    """Whatever the offsets hold, nothing before or behind out is written."""
+    n, K, N = 64, 256, 64
+    a, w, u, _ = rows_and_weights([30, 20, 14], K, N, up)
+    ws = moe.Workspace(256)
+    guard = 256
+    buf = torch.empty(n + 2 * guard, N, dtype=F16, device="cuda")
+    mats = [None if q is None else Mx4Mat(3, N, K, q.codes.data_ptr(), q.scales.data_ptr()) for q in (w, u)]
+    ref_of = [None if m is None else ctypes.addressof(m) for m in mats]
+    for bad in ([0, 30, 20, 64], [0, 30, 50, 100], [-5, 30, 50, 64], [3, 30, 50, 64], [0, 64, 0, 64],
+                [2 ** 31 - 1, -2 ** 31, 5, -1], [0, 0, 0, 2 ** 31 - 1], [-1, -1, -1, -1]):
+        buf.fill_(7.0)
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        assert moe.lib().moe_mx4_product(a.codes.data_ptr(), a.scales.data_ptr(), n, off.data_ptr(), 3, ref_of[0], ref_of[1],
+                                         buf[guard].data_ptr(), moe.F16, ws.buf.data_ptr(), ws.nbytes,
+                                         torch.cuda.current_stream().cuda_stream) == 0
+        assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_CHECK, bad
+        assert bool((buf[:guard] == 7).all()) and bool((buf[guard + n:] == 7).all()), bad
