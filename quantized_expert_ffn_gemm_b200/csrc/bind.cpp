@@ -120,6 +120,11 @@ struct Parts {
     return Tensor(std::move(impl));
   }
 };
+// A caller's buffer that a call has written: whoever saved it for a backward pass is told by its version. (Inference
+// tensors have none.)
+void written(const Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 void done(const char *fn, moe_status code) {
   if (code != MOE_OK) throw Status{fn, code};
 }
@@ -249,6 +254,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                         u.defined() ? u.data_ptr() : nullptr, type_code(ut),
                         rstd_y.defined() ? rstd_y.data_ptr<float>() : nullptr,
                         rstd_u.defined() ? rstd_u.data_ptr<float>() : nullptr, c.stream()));
+    if (a[10] != Py_None) written(r_out);
     return tuple_of(r_out, u, rstd_y, rstd_u);
   });
 }
@@ -349,6 +355,7 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     done("moe_dispatch", moe_dispatch(x.data_ptr(), type_code(x.scalar_type()), size32(T), size32(k), size32(H),
                                       row_of.data_ptr<int32_t>(), kept, rows.data_ptr(), c.stream()));
+    if (a[3] != Py_None) written(rows);
     return wrap(rows);
   });
 }

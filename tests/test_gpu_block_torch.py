@@ -42,3 +42,28 @@ def test_backward_of_a_gain_that_no_gradient_reaches(H):
     assert all(torch.equal(got[m], want[m]) for m in ("dr", "dy", "d_post_gain", "d_gate"))
     none = moe.block_norm_backward(dr[:0], None, r[:0], None, y[:0], ry[:0], pre_gain=gain, **args)
     assert bool((none["d_pre_gain"] == 0).all())
+
+
+def test_buffers_that_are_written_count_as_changed():
+    """An autograd function that saved r or rows is told that they were written."""
+    x = torch.randn(4, 128, device="cuda")
+    row_of = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    rows = torch.zeros(8, 128, device="cuda")
+    before = (x._version, rows._version, row_of._version)
+    moe.block_norm(x, r_out=x)
+    moe.dispatch(x, row_of, None, rows)
+    assert (x._version, rows._version, row_of._version) == (before[0] + 1, before[1] + 1, before[2])
+    with pytest.raises(moe.MoeError):  # refused: nothing was written
+        moe.block_norm(x, r_out=x, eps=-1.0)
+    assert x._version == before[0] + 1
+    leaf = torch.randn(4, 128, device="cuda", requires_grad=True)
+    r = leaf * 1.0
+    loss = (r * r).sum()  # saves r
+    with torch.no_grad():
+        moe.block_norm(r, r_out=r)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():  # tensors without such a count
+        free = torch.randn(4, 128, device="cuda")
+        moe.block_norm(free, r_out=free)
+    moe.block_norm(free, r_out=free)
