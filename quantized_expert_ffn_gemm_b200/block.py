@@ -7,6 +7,11 @@ contiguous CUDA tensors of one device; a call runs on that device's current stre
 current, and allocates its outputs unless they are given (a call's small ones as parts of one allocation). A
 tensor of another type, shape, layout or device than the call takes raises ValueError; what the library refuses
 raises MoeError.
+
+No call records an autograd graph: the gradients are entry points, to be called from a torch.autograd.Function. Where
+torch records and an input requires a gradient, a backward pass that comes to the call raises RuntimeError; a buffer
+to write (r_out, rows) goes by torch's rules for tensors changed in place. The codes of mx4_quantize are integers and
+take no gradient.
 """
 from __future__ import annotations
 

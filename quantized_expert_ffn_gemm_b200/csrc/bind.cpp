@@ -5,17 +5,24 @@
 //
 // A tensor of another type, shape, layout or device than the call takes raises ValueError, a status of the
 // library raises the package's MoeError. The call runs on its tensors' device and that device's current stream.
+//
+// No call records a gradient (the gradients are entry points of their own). Where torch records and an input requires one,
+// the results require one too, of a node that raises when a backward pass comes to it: as constants they would leave
+// their share out of it unseen.
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/VariableTypeUtils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/moe_ffn.h"
 
@@ -52,10 +59,11 @@ bool type_in(ScalarType t, Types k) {
   return k == kFloats ? type_code(t) >= 0 : k == kF32Only ? t == at::kFloat : k == kI32Only ? t == at::kInt : t == at::kByte;
 }
 
-// The device of a call and its guard: set by the first tensor.
+// The device of a call and its guard: set by the first tensor. And the inputs that require gradients.
 struct Call {
   int device = -1;
   std::optional<c10::cuda::CUDAGuard> guard;
+  std::vector<Tensor> grads;  // empty where torch does not record
 
   // a tensor argument, checked; nullptr for None where that is allowed
   const Tensor *tensor(const char *name, PyObject *o, Types types, int dim, bool optional = false) {
@@ -75,6 +83,7 @@ struct Call {
                     std::to_string(device));
     }
     if (!t.is_contiguous()) throw Refused(std::string(name) + ": not contiguous");
+    if (t.requires_grad() && c10::GradMode::is_enabled()) grads.push_back(t);
     return &t;
   }
   const Tensor *vector(const char *name, PyObject *o, Types types, int64_t n, bool optional = false) {
@@ -89,6 +98,26 @@ struct Call {
       throw Refused(std::string(name) + ": shape " + sizes_of(*t) + ", takes (" + std::to_string(n) + ", " +
                     std::to_string(m) + ")");
     return t;
+  }
+  // before a launch that writes a caller's buffer, all inputs read: torch's own rules for such a tensor
+  void may_write(const char *name, const Tensor &buffer) const {
+    if (!grads.empty() && buffer.is_inference()) throw Refused(std::string(name) + ": an inference tensor, with inputs that require gradients");
+    torch::autograd::check_inplace(buffer, !grads.empty());
+  }
+  // Behind a launch that wrote it: whoever saved it for a backward pass is told by its version. (Inference tensors
+  // have none.)
+  void written(const char *call, const char *says, const Tensor &buffer) const {
+    if (!buffer.is_inference()) torch::autograd::increment_version(buffer);
+    if (!grads.empty()) torch::autograd::rebase_history(buffer, no_graph(call, says));
+  }
+  void results(const char *call, const char *says, std::initializer_list<const Tensor *> outs) const {
+    if (grads.empty()) return;
+    for (const Tensor *t : outs)
+      if (t->defined()) torch::autograd::set_history(*t, no_graph(call, says));
+  }
+  std::shared_ptr<torch::autograd::Node> no_graph(const char *call, const char *says) const {
+    return {new torch::autograd::Error(std::string(call) + " records no graph: " + says, torch::autograd::collect_next_edges(grads)),
+            torch::autograd::deleteNode};
   }
   void *stream() const { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 };
@@ -120,11 +149,6 @@ struct Parts {
     return Tensor(std::move(impl));
   }
 };
-// A caller's buffer that a call has written: whoever saved it for a backward pass is told by its version. (Inference
-// tensors have none.)
-void written(const Tensor &t) {
-  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-}
 void done(const char *fn, moe_status code) {
   if (code != MOE_OK) throw Status{fn, code};
 }
@@ -238,6 +262,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       r_out = *c.matrix("r_out", a[10], kFloats, T, H);
       if (r_out.scalar_type() != r.scalar_type()) throw Refused("r_out: another type than r");
+      c.may_write("r_out", r_out);
     }
     Tensor u, rstd_y, rstd_u;
     const bool close = y && post_norm;
@@ -254,7 +279,10 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                         u.defined() ? u.data_ptr() : nullptr, type_code(ut),
                         rstd_y.defined() ? rstd_y.data_ptr<float>() : nullptr,
                         rstd_u.defined() ? rstd_u.data_ptr<float>() : nullptr, c.stream()));
-    if (a[10] != Py_None) written(r_out);
+    constexpr const char *kSays = "its gradient is block_norm_backward, for a torch.autograd.Function";
+    if (a[10] != Py_None) c.written("block_norm", kSays, r_out);
+    else c.results("block_norm", kSays, {&r_out});
+    c.results("block_norm", kSays, {&u, &rstd_y, &rstd_u});
     return tuple_of(r_out, u, rstd_y, rstd_u);
   });
 }
@@ -293,6 +321,7 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                  du ? ptr_as<float>(pre) : nullptr, dr.data_ptr(), y ? dy.data_ptr() : nullptr, p32(d_post),
                                  p32(d_gate), du ? p32(d_pre) : nullptr, ws.p, ws.n, c.stream()));
     if (pre && !du) d_pre.zero_();  // nothing reaches u: the library takes pre_gain with du alone
+    c.results("block_norm_backward", "second derivatives are not offered", {&dr, &dy, &d_post, &d_gate, &d_pre});
     return tuple_of(dr, dy, d_post, d_gate, d_pre);
   });
 }
@@ -352,10 +381,13 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       rows = *c.matrix("rows", a[3], kFloats, T * k, H);
       if (rows.scalar_type() != x.scalar_type()) throw Refused("rows: another type than x");
+      c.may_write("rows", rows);
     }
     done("moe_dispatch", moe_dispatch(x.data_ptr(), type_code(x.scalar_type()), size32(T), size32(k), size32(H),
                                       row_of.data_ptr<int32_t>(), kept, rows.data_ptr(), c.stream()));
-    if (a[3] != Py_None) written(rows);
+    constexpr const char *kSays = "its gradient is collect without weights, for a torch.autograd.Function";
+    if (a[3] != Py_None) c.written("dispatch", kSays, rows);
+    else c.results("dispatch", kSays, {&rows});
     return wrap(rows);
   });
 }
@@ -372,6 +404,7 @@ PyObject *collect(PyObject *, PyObject *const *a, Py_ssize_t n) {
     done("moe_collect", moe_collect(rows.data_ptr(), type_code(rows.scalar_type()), size32(T), size32(k), size32(H),
                                     row_of->data_ptr<int32_t>(), ptr_as<float>(w), ptr_as<float>(res), y.data_ptr(),
                                     type_code(yt), c.stream()));
+    c.results("collect", "its gradient is collect_backward, for a torch.autograd.Function", {&y});
     return wrap(y);
   });
 }
@@ -391,6 +424,7 @@ PyObject *collect_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
          moe_collect_backward(dy.data_ptr(), type_code(dy.scalar_type()), rows.data_ptr(), type_code(rows.scalar_type()),
                               size32(T), size32(k), size32(H), row_of->data_ptr<int32_t>(), ptr_as<float>(w), kept,
                               d_rows.data_ptr(), w ? d_w.data_ptr<float>() : nullptr, c.stream()));
+    c.results("collect_backward", "second derivatives are not offered", {&d_rows, &d_w});
     return tuple_of(d_rows, d_w);
   });
 }
