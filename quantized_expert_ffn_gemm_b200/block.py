@@ -65,7 +65,10 @@ def _load():
     moe.lib()  # says what to build where the library is missing
     if not os.path.exists(BIND_PATH):
         raise RuntimeError(f"{BIND_PATH} not found: build it with `python -m quantized_expert_ffn_gemm_b200.build`")
-    from . import _bind
+    from . import _bind, build
+    if _bind.built_for != build.bind_built_for():
+        raise RuntimeError(f"{BIND_PATH} was built for {_bind.built_for}, this is {build.bind_built_for()}: build it with "
+                           "`python -m quantized_expert_ffn_gemm_b200.build`")
     _bind.init_errors(moe.MoeError, torch.cuda.OutOfMemoryError)
     _b = _bind
     return _b

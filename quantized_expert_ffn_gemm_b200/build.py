@@ -39,16 +39,29 @@ def stale() -> bool:
     return _older(LIB, SOURCES + HEADERS)
 
 
+def bind_built_for() -> str:
+    """What a _bind.so belongs to: it uses torch's C++ interface, which each version changes, and Python's."""
+    import torch
+    return "torch %s, Python %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
+def bind_stale() -> bool:
+    if _older(BIND, [BIND_SOURCE, HEADERS[-1]]):
+        return True
+    with open(BIND, "rb") as f:  # the module's built_for, which ends with a zero
+        return bind_built_for().encode() + b"\0" not in f.read()
+
+
 def build_bind(force: bool = False, verbose: bool = False) -> str:
     """Compile and link _bind.so against torch and libmoe_ffn.so (found beside it at run time)."""
-    if not force and not _older(BIND, [BIND_SOURCE, HEADERS[-1]]):
+    if not force and not bind_stale():
         return BIND
     import torch
     tdir = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = BIND + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, '-DBUILT_FOR="%s"' % bind_built_for()]
     for inc in (os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
         cmd += ["-isystem", inc]

@@ -549,4 +549,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, g_methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__bind() {
+  PyObject *m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -158,3 +158,24 @@ def test_workspace_bytes_at_the_ends_of_the_sizes(lib):
     for T, k, E, H in ((1 << 32) + 1, 1, 1, 64), (1, 1, 1, (1 << 32) + 64), (1, (1 << 32) + 1, 4, 64), (1 << 31, 1, 1, 64), (
             -(1 << 32) + 1, 1, 1, 64):
         assert moe.block_workspace_bytes(T, k, E, H) == 0, (T, k, E, H)
+
+
+def test_a_binding_of_another_torch_is_built_again_and_not_called(lib, monkeypatch):
+    """_bind.so uses torch's C++ interface, which differs from version to version behind the same source."""
+    assert not moe_build.bind_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", torch.__version__ + ".later")
+        assert moe_build.bind_stale()
+        m.setattr(moe.block, "_b", None)
+        with pytest.raises(RuntimeError, match="build it with"):
+            moe.block_norm(torch.zeros(4, 128))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.block_norm(torch.zeros(4, 128))
+    with monkeypatch.context() as m:  # a shorter version's name is not found in a longer one's
+        m.setattr(moe_build, "bind_built_for", lambda: _bind_name()[:-1])
+        assert moe_build.bind_stale()
+
+
+def _bind_name():
+    import quantized_expert_ffn_gemm_b200._bind as b
+    return b.built_for
