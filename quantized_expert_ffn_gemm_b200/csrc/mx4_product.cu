@@ -123,6 +123,12 @@ __device__ __forceinline__ uint16_t cvt16(float v) {
   if constexpr (BF) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
   else return __half_as_ushort(__float2half_rn(v));
 }
+// gate / (1 + exp(-gate)) with e = exp(-|gate|), so that the divisor stays in (1, 2]: the fast division gives 0 from a
+// divisor of 2^126 on, which exp(-gate) passes at a gate of -87, where bf16 still holds the result.
+__device__ __forceinline__ float fast_silu(float gate) {
+  const float e = __expf(-fabsf(gate));
+  return __fdividef(gate < 0.0f ? gate * e : gate, 1.0f + e);
+}
 // n of a lane's values of C consecutive rows to those rows, N values apart. The type is known at compile time and a
 // whole chunk is stored without tests: with both decided value by value a store took 70 cycles. `top` becomes the largest
 // magnitude stored as fp16 (one instruction a value), so that what rounds to an infinity is seen once a launch.
@@ -489,7 +495,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             for (int j = 0; j < 8; ++j) {
               const float other = r[32 * j + lane], own = __uint_as_float(up_warp ? x[8 + j] : x[j]);
               const float gate = up_warp ? other : own, upv = up_warp ? own : other;
-              y[j] = __fdividef(gate, 1.0f + __expf(-gate)) * upv;
+              y[j] = fast_silu(gate) * upv;
             }
             store_rows<BF, 8>(up_warp ? o + 8 * (size_t)args.N : o, args.N, y, up_warp ? left - 8 : left, top);
           } else {

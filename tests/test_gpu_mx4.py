@@ -2,6 +2,7 @@
 
 Codes and scale bytes are equal bit for bit; reading back is exact."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -257,3 +258,23 @@ def test_product_with_bad_offsets_stays_in_its_rows(up):
                                          torch.cuda.current_stream().cuda_stream) == 0
         assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_CHECK, bad
         assert bool((buf[:guard] == 7).all()) and bool((buf[guard + n:] == 7).all()), bad
+
+
+@pytest.mark.parametrize("gate", [-64.0, -84.0, -86.0, -88.0, -92.0, -96.0, -0.5, 0.0, 2.0, 88.0, 96.0, 192.0])
+def test_silu_of_gates_far_from_zero(gate):
+    """silu(gate) up with exact gates and an up that brings the product back into bf16's middle range. CUDA's fast exp is good to
+    2 + 1.16 |x| steps of its fp32 result (2^-149 each where that is subnormal), its fast division to 2; two products."""
+    big = 2.0 ** 100 if gate < 0 else 1.0
+    parts = [math.copysign(p, gate) for p in (64.0, 32.0, 16.0, 8.0, 4.0, 2.0, 0.5) if int(2 * abs(gate)) & int(2 * p)]
+    if abs(gate) >= 128:
+        parts.append(math.copysign(128.0, gate))
+    parts = (parts + [0.0] * 6)[:6]
+    assert sum(parts) == gate
+    a = moe.mx4_quantize(torch.cat([block_values(*[1.0] * 6)] * 3).cuda())
+    w = moe.mx4_quantize(block_values(*parts).expand(64, -1).contiguous()[None].cuda())
+    u = moe.mx4_quantize(block_values(big, 0, 0, 0, 0, 0).expand(64, -1).contiguous()[None].cuda())
+    ws = moe.Workspace(256)
+    got = moe.mx4_product(a, w, up=u, dtype=BF16, ws=ws)
+    want = torch.full((3, 64), gate / (1 + math.exp(-gate)) * big, dtype=torch.float64)
+    rel = (2 + 1.16 * abs(gate) + 4) * max(2.0 ** -23, 2.0 ** -149 / math.exp(-abs(gate)) if gate < 0 else 0)
+    close(got, want, rel * want.abs() + rounded(want, BF16), "silu")
