@@ -7,7 +7,7 @@
 #include <mutex>
 #include <vector>
 
-#include "common.cuh"
+#include "block.cuh"
 
 namespace moe {
 
@@ -32,7 +32,7 @@ cudaEvent_t take_event() {
   }
   return e;
 }
-const char *const kKernelNames[KID_COUNT] = {
+const char *const kKernelNames[KID_ALL] = {
     "router_decode", "router_gemm", "topk", "perm_hist", "perm_scan", "perm_scatter", "perm_gather", "combine", "rmsnorm", "dequant_rows", "dec_units", "dec_gate_up", "dec_down",
     "tile_list", "gemm_gate_up", "gemm_down", "router_split", "router_tc", "decode_fused", "mmq_quant",
     "mmq_gate_up", "mid_plan", "mid_expert", "mid_combine", "block_norm", "block_norm_grad",
@@ -587,7 +587,7 @@ moe_status moe_timing_enable(int32_t on) {
 }
 
 moe_status moe_timing_read(int32_t kernel, double *total_ms, int32_t *launches) {
-  if (kernel < 0 || kernel >= KID_COUNT || !total_ms || !launches) return MOE_ERR_INVALID_ARG;
+  if (kernel < 0 || kernel >= KID_ALL || !total_ms || !launches) return MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_tmu);
   double tot = 0.0;
   int n = 0;
@@ -604,10 +604,10 @@ moe_status moe_timing_read(int32_t kernel, double *total_ms, int32_t *launches) 
   return MOE_OK;
 }
 
-int32_t moe_kernel_count(void) { return KID_COUNT; }
+int32_t moe_kernel_count(void) { return KID_ALL; }
 
 const char *moe_kernel_name(int32_t kernel) {
-  return (kernel >= 0 && kernel < KID_COUNT) ? kKernelNames[kernel] : nullptr;
+  return (kernel >= 0 && kernel < KID_ALL) ? kKernelNames[kernel] : nullptr;
 }
 
 moe_status moe_test_wait_timeout(void *ws, size_t ws_bytes, int32_t limit_ms, void *stream) {

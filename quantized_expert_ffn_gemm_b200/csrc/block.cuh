@@ -6,6 +6,12 @@
 
 namespace moe {
 
+// the block operators' kernels, numbered behind the layers' (common.cuh) for the timing hook
+enum BlockKernelId {
+  KID_BLOCK_NORM = KID_COUNT, KID_BLOCK_NORM_GRAD, KID_BLOCK_NORM_GAIN, KID_PAIR_HIST, KID_PAIR_SCAN, KID_PAIR_PLACE,
+  KID_DISPATCH, KID_COLLECT, KID_COLLECT_GRAD, KID_MX4_QUANTIZE, KID_MX4_DEQUANTIZE, KID_MX4_PRODUCT, KID_ALL
+};
+
 // The kernels' type codes: the public ones, and fp32 whose base is 32-byte aligned, which moves eight values
 // in one access. Two 16-byte accesses 32 bytes apart between lanes touch each 32-byte sector twice.
 constexpr int kF32Wide = 3;
