@@ -293,18 +293,19 @@ moe_status moe_router_topk_static(const uint16_t *x, int32_t T, int32_t H, const
                                   int32_t E, int32_t k, int32_t *idx, float *w, float *logits_opt, void *stream);
 
 /* ------------------------------------------------------------------ block operators
- * What a block needs around its experts, for serving and for training: the norms that close one
- * block and open the next, the (token, slot) pairs sorted by expert and collected again, each with
- * its gradient, and MXFP4 rows with their product per expert. Values are fp32, fp16 or bf16 (a
+ * What a block needs around its experts: the norms that close one block and open the next and the
+ * (token, slot) pairs sorted by expert and collected again, each with its gradient, and MXFP4 rows
+ * with their product per expert (forward alone: these have no gradient). Values are fp32, fp16 or bf16 (a
  * MOE_F32 / MOE_F16 / MOE_BF16 argument names the type of the tensor before it); gains, gates,
  * routing weights and statistics are fp32, sums are carried in fp32 and a result is rounded once, to
  * nearest even (beyond fp16's range to +-inf; of these calls moe_mx4_product alone records that).
  * Results are the same in every run. The conventions above hold; shape rules: H, K and N multiples
  * of 64 up to 16384 (a multiple of 32 gives MOE_ERR_UNSUPPORTED, anything else MOE_ERR_INVALID_ARG),
- * 1 <= k <= min(E, 32), E <= 4096, T * k < 2^31. Outputs do not overlap inputs unless said so. Router
- * weights Wr that one of these calls writes (moe_mx4_dequantize apart) are safe for a router or layer
- * call only after a synchronisation or a plainly launched kernel between the two: these kernels let
- * their dependents start at their entry. */
+ * 1 <= k <= min(E, 32), E <= 4096, T * k < 2^31. Outputs do not overlap inputs unless said so. The
+ * kernels let their dependents start at their entry, but for those of moe_mx4_dequantize and
+ * moe_mx4_product, whose dependents start when they end. Router weights Wr that one of the former
+ * calls writes are therefore safe for a router or layer call only after a synchronisation or a
+ * plainly launched kernel between the two. */
 enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 };
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
 

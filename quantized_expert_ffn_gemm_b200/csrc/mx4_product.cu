@@ -587,8 +587,9 @@ cudaError_t launch_tiles(const Mx4ProductArgs &p, cudaStream_t s) {
   const cudaError_t e = smem_limit_once(mx4_product_kernel<UP, BF, NT>, MxCfg<NT>::smem(kMaxE, UP));
   if (e != cudaSuccess) return e;
   KTimer kt_(KID_MX4_PRODUCT, s);
-  // A short product begins while its predecessor ends (four tokens: 0.5 us). A long one gains nothing, and with
-  // its blocks waiting beside the quantiser's the two took 173-180 us for 8192 tokens, not 172.
+  // A short product begins while its predecessor ends (40 rows, four tokens: 0.5 us). A long one gains nothing, and with
+  // its blocks waiting beside the quantiser's the two took 173-180 us for 81,920 rows, not 172. The border between
+  // the two measurements is not measured.
   if (p.n_rows <= 4096)
     return launch_pdl(mx4_product_kernel<UP, BF, NT>, dim3(grid), dim3(MxCfg<NT>::kThreads), MxCfg<NT>::smem(p.E, UP), s, ta, tw, tu, a);
   mx4_product_kernel<UP, BF, NT><<<grid, MxCfg<NT>::kThreads, MxCfg<NT>::smem(p.E, UP), s>>>(ta, tw, tu, a);
@@ -598,7 +599,8 @@ cudaError_t launch_tiles(const Mx4ProductArgs &p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mx4_product(const Mx4ProductArgs &p, cudaStream_t s) {
-  // Rows of a tile: 192 where groups are long (8192 tokens over 512 experts, 160 rows each, with the quantiser:
+  // Rows of a tile, by the mean over all experts (the host does not know how many are idle): 192 where
+  // groups are long (8192 tokens over 512 experts, 160 rows each, with the quantiser:
   // 156 us, 185 with 96), else 96: a stage is smaller and more are in flight, and four accumulators leave
   // short tiles' epilogues behind (2048 tokens, down, 40 rows each: 67.8 us, 72.2 with 192; ten rows of
   // one token: 12.3 us cold, 13.8).
