@@ -66,8 +66,9 @@ def _load():
     if not os.path.exists(BIND_PATH):
         raise RuntimeError(f"{BIND_PATH} not found: build it with `python -m quantized_expert_ffn_gemm_b200.build`")
     from . import _bind, build
-    if _bind.built_for != build.bind_built_for():
-        raise RuntimeError(f"{BIND_PATH} was built for {_bind.built_for}, this is {build.bind_built_for()}: build it with "
+    built_for, here = getattr(_bind, "built_for", "an older tree"), build.bind_built_for()
+    if built_for != here:
+        raise RuntimeError(f"{BIND_PATH} was built for {built_for}, this is {here}: build it with "
                            "`python -m quantized_expert_ffn_gemm_b200.build`")
     _bind.init_errors(moe.MoeError, torch.cuda.OutOfMemoryError)
     _b = _bind

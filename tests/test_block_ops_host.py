@@ -171,6 +171,12 @@ def test_a_binding_of_another_torch_is_built_again_and_not_called(lib, monkeypat
             moe.block_norm(torch.zeros(4, 128))
     with pytest.raises(ValueError, match="CUDA"):
         moe.block_norm(torch.zeros(4, 128))
+    with monkeypatch.context() as m:  # one that does not say what it was built for
+        import quantized_expert_ffn_gemm_b200._bind as b
+        m.delattr(b, "built_for")
+        m.setattr(moe.block, "_b", None)
+        with pytest.raises(RuntimeError, match="build it with"):
+            moe.block_norm(torch.zeros(4, 128))
     with monkeypatch.context() as m:  # a shorter version's name is not found in a longer one's
         m.setattr(moe_build, "bind_built_for", lambda: _bind_name()[:-1])
         assert moe_build.bind_stale()
